@@ -9,78 +9,14 @@
 #include <mutex>
 
 #include "goldwkv.h"
+#include "api_checks.h"
 #include "internal.h"
 #include "backward.h"
 #include "gold.h"
 
 namespace {
 
-constexpr int kHeadSizeApi = 64;  // D: the only head size the kernels are built for
-constexpr size_t kStatusBytes = 256;  // device status word at the start of the workspace
-// Bounded waits inside the chunked kernel: SM cycles (about a second at 1.9 GHz).
-constexpr long long kSpinBudget = 2000000000LL;
-
-struct Span {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-Span span(const void* p, size_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Span{a, a + bytes};
-}
-
-bool overlaps(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Host-side fault injection for tests of the error paths: GOLDWKV_FAULT=launch makes the
-// entry points report a failed launch without launching anything.
-bool injected(const char* what) {
-    const char* f = getenv("GOLDWKV_FAULT");
-    return f != nullptr && strcmp(f, what) == 0;
-}
-
-// p must be memory the current device can address as device memory.
-bool on_current_device(const void* p, int dev) {
-    cudaPointerAttributes a;
-    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return false;
-    }
-    if (a.type == cudaMemoryTypeDevice) return a.device == dev;
-    if (a.type == cudaMemoryTypeManaged) return true;
-    return false;
-}
-
-struct Buf {
-    const void* p;
-    size_t bytes;
-    bool required;
-};
-
-// Common pointer checks: required non-null, 16-byte aligned, on the current device.
-wkv_status check_bufs(const Buf* bufs, int n) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return WKV_ERR_CUDA;
-    }
-    for (int i = 0; i < n; ++i) {
-        if (bufs[i].p == nullptr) {
-            if (bufs[i].required) return WKV_ERR_INVALID_ARG;
-            continue;
-        }
-        if (!aligned16(bufs[i].p)) return WKV_ERR_INVALID_ARG;
-        if (!on_current_device(bufs[i].p, dev)) return WKV_ERR_INVALID_ARG;
-    }
-    return WKV_OK;
-}
-
-wkv_status from_cuda(cudaError_t e) { return e == cudaSuccess ? WKV_OK : WKV_ERR_CUDA; }
-
-size_t io_size(wkv_dtype io) { return io == WKV_BF16 ? 2 : 4; }
-
-bool valid_io(wkv_dtype io) { return io == WKV_F32 || io == WKV_BF16; }
+using namespace goldwkv::api;
 
 // Output stage after the recurrence: none, LayerNorm over a token's H*D channels, or
 // base Finch's per-head GroupNorm times an optional gate.
@@ -139,8 +75,6 @@ bool use_chunked(wkv_dtype io, wkv_algo algo) {
     if (algo == WKV_ALGO_RECURRENT) return false;
     return io == WKV_BF16;
 }
-
-size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 constexpr int kChunk = 64;          // tokens per chunk of the chunked kernels
 constexpr int kSmCountDefault = 148;   // SMs of a full B200, if the device cannot be asked
