@@ -357,6 +357,96 @@ wkv_status gold_decompress(const void *x0, const void *c, const void *w_ku, cons
                            float eps, void *kd, long N, int D, int Dc, void *workspace,
                            size_t workspace_bytes, void *stream);
 
+/*
+ * The gated delta rule: the other recurrence of linear-attention layers, over the same state as
+ * the WKV recurrence above.  Per batch row b and value head h, a D x D fp32 state S (rows i key
+ * channels, columns j value channels), one decay logit omega and one write strength beta a
+ * token; for each token t, with w_t = exp(-exp(omega_t)):
+ *     e_t[j]  = v_t[j] - w_t sum_i S[i][j] k_t[i]        (what the decayed state lacks of v_t at k_t)
+ *     S[i][j] = w_t S[i][j] + beta_t k_t[i] e_t[j]
+ *     y_t[j]  = scale sum_i S[i][j] q_t[i]               (reads the state after its update)
+ * Layouts, row-major and dense, of the I/O type `io` unless said:
+ *   q, k        [B][T][HK][D]   value head h reads key head h / (H / HK); HK divides H
+ *   v, y        [B][T][H][D]
+ *   omega, beta [B][T][H]       omega = -inf: no decay; +inf: the state is forgotten.  A token
+ *                               with beta = 0 writes nothing, and with omega = -inf as well it
+ *                               leaves the state as it is (padding; its other inputs finite)
+ *   state       [B][H][D][D] fp32
+ * Keys are taken as given: the rule is stable for |k_t| <= 1 and beta in [0, 2], which is the
+ * caller's to see to (unit-length keys).  scale must be finite.  The conventions at the top of
+ * this file hold (device pointers, no allocation, errors before any launch); 16-byte alignment
+ * is asked of every pointer but omega, beta and their gradients, which need that of their type.
+ *
+ * gated_delta_prefill: T tokens from state_in (NULL: zero).  state_out [B][H][D][D] or NULL (not
+ * written); it may equal state_in.  No other overlap of an output.  T == 0: state_out receives
+ * state_in, or zeros.  workspace: at least gated_delta_prefill_workspace_bytes(...) bytes (may be
+ * NULL when that is 0).
+ */
+size_t gated_delta_prefill_workspace_bytes(int B, int T, int H, int HK, int D, wkv_dtype io);
+wkv_status gated_delta_prefill(const void *q, const void *k, const void *v, const void *omega,
+                               const void *beta, float scale, const float *state_in,
+                               float *state_out, void *y, int B, int T, int H, int HK, int D,
+                               wkv_dtype io, void *workspace, size_t workspace_bytes, void *stream);
+
+/* gated_delta_decode_step: one token (the layouts above without T), the state updated in place.
+ * One launch; no workspace. */
+wkv_status gated_delta_decode_step(const void *q, const void *k, const void *v, const void *omega,
+                                   const void *beta, float scale, float *state, void *y, int B,
+                                   int H, int HK, int D, wkv_dtype io, void *stream);
+
+/*
+ * gated_delta_backward: the gradients of a loss with respect to every input of
+ * gated_delta_prefill, given dy [B][T][H][D] io and dstate_out [B][H][D][D] fp32 (the final
+ * state's gradient, NULL: zero).  Outputs: dq, dk [B][T][HK][D] io (each key head's the sum over
+ * its value heads), dv [B][T][H][D] io, domega, dbeta [B][T][H] io, dstate_in [B][H][D][D] fp32
+ * or NULL (not computed).  No output may overlap an input, another output or the workspace.
+ * T == 0: dstate_in = dstate_out, or zeros.  The same inputs give the same bits (no atomics).
+ */
+size_t gated_delta_backward_workspace_bytes(int B, int T, int H, int HK, int D, wkv_dtype io);
+wkv_status gated_delta_backward(const void *q, const void *k, const void *v, const void *omega,
+                                const void *beta, float scale, const float *state_in,
+                                const void *dy, const float *dstate_out, void *dq, void *dk,
+                                void *dv, void *domega, void *dbeta, float *dstate_in, int B,
+                                int T, int H, int HK, int D, wkv_dtype io, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* Activations of group_norm_act. */
+typedef enum wkv_act {
+    WKV_ACT_NONE = 0,
+    WKV_ACT_SILU = 1           /* x / (1 + exp(-x))                                       */
+} wkv_act;
+
+/*
+ * Group norm with an activation, channels last: the output stage of a recurrent layer on its
+ * own, for either recurrence, with a gradient.  x [N][L][C] io, C = groups * per: for each n
+ * and group of `per` adjacent channels, mean and biased variance over its L positions:
+ *     z = (x - mean) / sqrt(var + eps) * gamma + beta
+ *     y = act(z)              without a gate
+ *     y = z * act(gate)       with one
+ * A layer's per-head norm of every token is N = tokens, L = 1, groups = heads.
+ *   gamma, beta [C] fp32;  gate [N][L][C] io or NULL;  y [N][L][C] io;  eps > 0.
+ *   y may not overlap an input or the workspace.  N == 0 or L == 0 is an empty problem.
+ *   workspace: at least group_norm_act_workspace_bytes(...) bytes (0 where L == 1); no initial
+ *   contents needed.
+ */
+size_t group_norm_act_workspace_bytes(long N, long L, int C, int groups, wkv_dtype io);
+wkv_status group_norm_act(const void *x, const float *gamma, const float *beta, float eps,
+                          wkv_act act, const void *gate, void *y, long N, long L, int C,
+                          int groups, wkv_dtype io, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/* group_norm_act_backward: gradients for dy [N][L][C] io.  dx [N][L][C] io, dgamma, dbeta [C]
+ * fp32 (summed over n and positions, overwritten; zeros for an empty problem), dgate
+ * [N][L][C] io (required with a gate, else NULL).  The statistics are formed again from x.  No
+ * output may overlap an input, another output or the workspace.  The same inputs give the same
+ * bits. */
+size_t group_norm_act_backward_workspace_bytes(long N, long L, int C, int groups, wkv_dtype io);
+wkv_status group_norm_act_backward(const void *x, const float *gamma, const float *beta, float eps,
+                                   wkv_act act, const void *gate, const void *dy, void *dx,
+                                   float *dgamma, float *dbeta, void *dgate, long N, long L, int C,
+                                   int groups, wkv_dtype io, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
 /* Size of the scratch array built into the library for wkv6_prefill_static, per device. */
 #define WKV6_STATIC_SCRATCH_BYTES ((size_t)8 << 20)
 

@@ -95,6 +95,25 @@ def load(path: Path | str | None = None):
     L.gold_compress.restype = i
     L.gold_decompress.argtypes = [vp, vp, vp, vp, ctypes.c_float, vp, ctypes.c_long, i, i, vp, sz, vp]
     L.gold_decompress.restype = i
+    f, lg = ctypes.c_float, ctypes.c_long
+    L.gated_delta_prefill_workspace_bytes.argtypes = [i] * 6
+    L.gated_delta_prefill_workspace_bytes.restype = sz
+    L.gated_delta_prefill.argtypes = [vp] * 5 + [f] + [vp] * 3 + [i] * 6 + [vp, sz, vp]
+    L.gated_delta_prefill.restype = i
+    L.gated_delta_decode_step.argtypes = [vp] * 5 + [f] + [vp] * 2 + [i] * 5 + [vp]
+    L.gated_delta_decode_step.restype = i
+    L.gated_delta_backward_workspace_bytes.argtypes = [i] * 6
+    L.gated_delta_backward_workspace_bytes.restype = sz
+    L.gated_delta_backward.argtypes = [vp] * 5 + [f] + [vp] * 9 + [i] * 6 + [vp, sz, vp]
+    L.gated_delta_backward.restype = i
+    L.group_norm_act_workspace_bytes.argtypes = [lg, lg, i, i, i]
+    L.group_norm_act_workspace_bytes.restype = sz
+    L.group_norm_act.argtypes = [vp] * 3 + [f, i] + [vp] * 2 + [lg, lg, i, i, i, vp, sz, vp]
+    L.group_norm_act.restype = i
+    L.group_norm_act_backward_workspace_bytes.argtypes = [lg, lg, i, i, i]
+    L.group_norm_act_backward_workspace_bytes.restype = sz
+    L.group_norm_act_backward.argtypes = [vp] * 3 + [f, i] + [vp] * 6 + [lg, lg, i, i, i, vp, sz, vp]
+    L.group_norm_act_backward.restype = i
     L.wkv6_workspace_status.argtypes = [vp, vp]
     L.wkv6_workspace_status.restype = i
     L.wkv6_status_string.argtypes = [i]
@@ -616,3 +635,210 @@ def wkv6c2_backward(r, k, v, omega, state_in, dy, dstate_out=None, *, want_dstat
                                ws_bytes, _stream_ptr(dev, stream))
     _raise("wkv6c2_backward", st)
     return dr, dk, dv, dom, dup, ds_in
+
+
+# ------------------------------------------------------------------ the gated delta rule
+
+ACTS = {"none": 0, "silu": 1}
+
+
+def _need_cuda(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors (no CPU implementation)")
+
+
+def _gdr_args(q, k, v, omega, beta, lead):
+    """Checks of q, k [*lead, HK, D], v [*lead, H, D], omega, beta [*lead, H]; (H, HK, D)."""
+    _need_cuda(q, "q")
+    if q.dim() != lead + 2 or not isinstance(v, torch.Tensor) or v.dim() != lead + 2:
+        raise ValueError("q and v must be " + ("[B, T, heads, D]" if lead == 2 else "[B, heads, D]"))
+    front, HK, D, H = tuple(q.shape[:lead]), q.shape[-2], q.shape[-1], v.shape[-2]
+    if H and (HK == 0 or H % HK):
+        raise ValueError(f"the {H} value heads must be a multiple of the {HK} key heads")
+    dev, dt = q.device, q.dtype
+    _check("q", q, dev, dt, (*front, HK, D))
+    _check("k", k, dev, dt, (*front, HK, D))
+    _check("v", v, dev, dt, (*front, H, D))
+    _check("omega", omega, dev, dt, (*front, H))
+    _check("beta", beta, dev, dt, (*front, H))
+    return H, HK, D
+
+
+def _ws_bytes(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def gated_delta_prefill_workspace_bytes(B, T, H, HK, D, io_dtype) -> int:
+    return int(load().gated_delta_prefill_workspace_bytes(B, T, H, HK, D, _io(io_dtype)))
+
+
+def gated_delta_backward_workspace_bytes(B, T, H, HK, D, io_dtype) -> int:
+    return int(load().gated_delta_backward_workspace_bytes(B, T, H, HK, D, _io(io_dtype)))
+
+
+def gated_delta_prefill(q, k, v, omega, beta, state_in=None, *, scale=1.0, y=None, state_out=None,
+                        want_state=True, workspace=None, stream=None):
+    """The gated delta rule over T tokens (include/goldwkv.h, gated_delta_prefill): q, k
+    [B, T, HK, D], v [B, T, H, D], omega, beta [B, T, H], all fp32 or bf16; value head h reads
+    key head h // (H // HK).  ``state_in`` [B, H, D, D] fp32 or None (zero).
+
+    Returns (y [B, T, H, D], state_out); state_out is None when ``want_state`` is False and no
+    ``state_out`` tensor was given.  ``state_out`` may be ``state_in`` (in-place update).
+    """
+    L = load()
+    H, HK, D = _gdr_args(q, k, v, omega, beta, 2)
+    B, T = q.shape[:2]
+    dev, dt = q.device, q.dtype
+    if state_in is not None:
+        _check("state_in", state_in, dev, torch.float32, (B, H, D, D))
+    if y is None:
+        y = torch.empty((B, T, H, D), dtype=dt, device=dev)
+    else:
+        _check("y", y, dev, dt, (B, T, H, D))
+    if state_out is not None:
+        _check("state_out", state_out, dev, torch.float32, (B, H, D, D))
+    elif want_state:
+        state_out = torch.empty((B, H, D, D), dtype=torch.float32, device=dev)
+    io = _io(dt)
+    need = int(L.gated_delta_prefill_workspace_bytes(B, T, H, HK, D, io))
+    if workspace is None and need > 0:
+        workspace = new_workspace(need, dev)   # zero: status word
+    with torch.cuda.device(dev):
+        st = L.gated_delta_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(omega), _ptr(beta), float(scale),
+                                   _ptr(state_in), _ptr(state_out), _ptr(y), B, T, H, HK, D, io,
+                                   _ptr(workspace), _ws_bytes(workspace), _stream_ptr(dev, stream))
+    _raise("gated_delta_prefill", st)
+    return y, state_out
+
+
+def gated_delta_decode_step(q, k, v, omega, beta, state, *, scale=1.0, y=None, stream=None):
+    """One token of the gated delta rule: q, k [B, HK, D], v [B, H, D], omega, beta [B, H];
+    ``state`` [B, H, D, D] fp32 is updated in place.  Returns y [B, H, D]."""
+    L = load()
+    H, HK, D = _gdr_args(q, k, v, omega, beta, 1)
+    B = q.shape[0]
+    dev, dt = q.device, q.dtype
+    _check("state", state, dev, torch.float32, (B, H, D, D))
+    if y is None:
+        y = torch.empty((B, H, D), dtype=dt, device=dev)
+    else:
+        _check("y", y, dev, dt, (B, H, D))
+    with torch.cuda.device(dev):
+        st = L.gated_delta_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(omega), _ptr(beta),
+                                       float(scale), _ptr(state), _ptr(y), B, H, HK, D, _io(dt),
+                                       _stream_ptr(dev, stream))
+    _raise("gated_delta_decode_step", st)
+    return y
+
+
+def gated_delta_backward(q, k, v, omega, beta, state_in, dy, dstate_out=None, *, scale=1.0,
+                         want_dstate_in=True, workspace=None, stream=None):
+    """Gradients of gated_delta_prefill given dy [B, T, H, D] (dtype of q) and the final
+    state's gradient dstate_out [B, H, D, D] fp32 (None: zero).  Returns (dq, dk, dv, domega,
+    dbeta, dstate_in [B, H, D, D] fp32 or None)."""
+    L = load()
+    H, HK, D = _gdr_args(q, k, v, omega, beta, 2)
+    B, T = q.shape[:2]
+    dev, dt = q.device, q.dtype
+    _check("dy", dy, dev, dt, (B, T, H, D))
+    for name, t in (("state_in", state_in), ("dstate_out", dstate_out)):
+        if t is not None:
+            _check(name, t, dev, torch.float32, (B, H, D, D))
+    dq, dk = torch.empty_like(q), torch.empty_like(k)
+    dv, domega, dbeta = torch.empty_like(v), torch.empty_like(omega), torch.empty_like(beta)
+    ds_in = torch.empty((B, H, D, D), dtype=torch.float32, device=dev) if want_dstate_in else None
+    io = _io(dt)
+    need = int(L.gated_delta_backward_workspace_bytes(B, T, H, HK, D, io))
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        st = L.gated_delta_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(omega), _ptr(beta), float(scale),
+                                    _ptr(state_in), _ptr(dy), _ptr(dstate_out), _ptr(dq), _ptr(dk),
+                                    _ptr(dv), _ptr(domega), _ptr(dbeta), _ptr(ds_in), B, T, H, HK,
+                                    D, io, _ptr(workspace), _ws_bytes(workspace),
+                                    _stream_ptr(dev, stream))
+    _raise("gated_delta_backward", st)
+    return dq, dk, dv, domega, dbeta, ds_in
+
+
+# ------------------------------------------------------------------ group norm with an activation
+
+def _gn_sizes(x, gamma, beta, groups, act, gate):
+    """Checks of x [N, ..., C] and its parameters; (N, L, C)."""
+    _need_cuda(x, "x")
+    if x.dim() < 2:
+        raise ValueError("x must be [N, ..., C]")
+    N, C = x.shape[0], x.shape[-1]
+    if C == 0 or groups <= 0 or C % groups:
+        raise ValueError(f"the {C} channels must be a positive multiple of groups ({groups})")
+    if act not in ACTS:
+        raise ValueError(f"unknown activation {act!r}; expected one of {sorted(ACTS)}")
+    L = 1
+    for n in x.shape[1:-1]:
+        L *= n
+    dev, dt = x.device, x.dtype
+    _check("x", x, dev, dt)
+    _check("gamma", gamma, dev, torch.float32, (C,))
+    _check("beta", beta, dev, torch.float32, (C,))
+    if gate is not None:
+        _check("gate", gate, dev, dt, tuple(x.shape))
+    return N, L, C
+
+
+def group_norm_act(x, gamma, beta, eps=1e-5, *, groups, act="silu", gate=None, y=None,
+                   workspace=None, stream=None):
+    """Group norm over channels-last x [N, ..., C] (fp32 or bf16) with an activation
+    (include/goldwkv.h, group_norm_act): mean and variance for each n and group of C / groups
+    adjacent channels over all positions between, gamma and beta [C] fp32, then ``act`` ("silu"
+    or "none") of the result, or with ``gate`` (like x) the result times act(gate).  Every
+    token's heads on their own: x [tokens, C], groups = heads.  Returns y."""
+    L_ = load()
+    N, L, C = _gn_sizes(x, gamma, beta, groups, act, gate)
+    dev, dt = x.device, x.dtype
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _check("y", y, dev, dt, tuple(x.shape))
+    io = _io(dt)
+    need = int(L_.group_norm_act_workspace_bytes(N, L, C, groups, io)) if L != 1 else 0
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        st = L_.group_norm_act(_ptr(x), _ptr(gamma), _ptr(beta), float(eps), ACTS[act], _ptr(gate),
+                               _ptr(y), N, L, C, groups, io, _ptr(workspace), _ws_bytes(workspace),
+                               _stream_ptr(dev, stream))
+    _raise("group_norm_act", st)
+    return y
+
+
+def group_norm_act_backward(x, gamma, beta, eps, dy, *, groups, act="silu", gate=None,
+                            workspace=None, stream=None):
+    """Gradients of group_norm_act for dy (like x): (dx, dgamma [C] fp32, dbeta [C] fp32, dgate
+    or None).  The statistics are formed again from x."""
+    L_ = load()
+    N, L, C = _gn_sizes(x, gamma, beta, groups, act, gate)
+    dev, dt = x.device, x.dtype
+    _check("dy", dy, dev, dt, tuple(x.shape))
+    dx = torch.empty_like(x)
+    dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(beta)
+    dgate = None if gate is None else torch.empty_like(x)
+    io = _io(dt)
+    need = int(L_.group_norm_act_backward_workspace_bytes(N, L, C, groups, io))
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        st = L_.group_norm_act_backward(_ptr(x), _ptr(gamma), _ptr(beta), float(eps), ACTS[act],
+                                        _ptr(gate), _ptr(dy), _ptr(dx), _ptr(dgamma), _ptr(dbeta),
+                                        _ptr(dgate), N, L, C, groups, io, _ptr(workspace),
+                                        _ws_bytes(workspace), _stream_ptr(dev, stream))
+    _raise("group_norm_act_backward", st)
+    return dx, dgamma, dbeta, dgate
+
+
+def group_norm_act_workspace_bytes(N, L, C, groups, io_dtype, backward=False) -> int:
+    """Bytes of workspace group_norm_act (or its backward) needs for x [N, L positions, C]."""
+    L_ = load()
+    fn = L_.group_norm_act_backward_workspace_bytes if backward else L_.group_norm_act_workspace_bytes
+    return int(fn(N, L, C, groups, _io(io_dtype)))
