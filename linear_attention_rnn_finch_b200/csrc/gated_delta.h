@@ -23,6 +23,9 @@ struct GdrIn {
 cudaError_t launch_gdr_recurrent(const GdrIn& in, const float* s_in, float* s_out, void* y,
                                  bool bf16, cudaStream_t st);
 
+// Chunked on tensor cores, bf16 I/O.  s_out may equal s_in or be null; s_in null: zero.
+cudaError_t launch_gdr_chunked(const GdrIn& in, const float* s_in, float* s_out, void* y, cudaStream_t st);
+
 // One token, the state updated in place (T is ignored).
 cudaError_t launch_gdr_decode(const GdrIn& in, float* state, void* y, bool bf16, cudaStream_t st);
 

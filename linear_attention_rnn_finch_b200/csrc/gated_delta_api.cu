@@ -104,7 +104,8 @@ wkv_status gated_delta_prefill(const void* q, const void* k, const void* v, cons
     if (injected("launch")) return WKV_ERR_CUDA;
     if (!tokens) return pass_state(state_out, state_in, sb, st);
     const goldwkv::GdrIn in{q, k, v, omega, beta, scale, B, T, H, HK};
-    return from_cuda(goldwkv::launch_gdr_recurrent(in, state_in, state_out, y, io == WKV_BF16, st));
+    if (io == WKV_BF16) return from_cuda(goldwkv::launch_gdr_chunked(in, state_in, state_out, y, st));
+    return from_cuda(goldwkv::launch_gdr_recurrent(in, state_in, state_out, y, false, st));
 }
 
 wkv_status gated_delta_decode_step(const void* q, const void* k, const void* v, const void* omega,

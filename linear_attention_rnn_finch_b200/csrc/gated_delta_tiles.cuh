@@ -1,0 +1,235 @@
+// What the tensor-core kernels of the gated delta rule share: loading blocks of 64 tokens and
+// preparing what depends on no state.
+//
+// A block is cut into sub-chunks of 16 tokens.  Inside one, with L_t the sum of log w up to t,
+// g = e^L, D_ts = e^(L_t - L_s) <= 1 for t >= s, and the entering state S (64 x 64):
+//     M = strictly lower (K K^T . D),  T = (I + M b)^-1,  P = scale lower (Q K^T . D),
+//     F = V - g (K S),  E = T F,  Y = scale g (Q S) + P (b E),
+//     S+ = g_16 S + K^T (b to_end E),   to_end_t = e^(L_16 - L_t).
+// 16, not 64: the products with S, Q S, K^T E cost the same per token whatever the length of a
+// sub-chunk, while those with T and P and the inverse grow with it (per 64 tokens and 16 value
+// columns 240 matrix instructions instead of 312, an inverse without block products), and the
+// longer chain of dependent products is hidden by the other CTA of the SM.
+//
+// Four warps (the chain) own 16 value columns each and keep S^T in registers as accumulators
+// (rows value columns, columns key channels).  Everything transposed (F^T = V^T - g S^T K^T,
+// E^T = F^T T^T, ...) each result has the layout of the next product's A operand, so a block
+// passes through them without shared memory or barriers between its products.  Four more warps
+// (the preparation) work one block ahead: they issue the copies of the block after it, and
+// form decays, T and P of one sub-chunk each.  The two halves meet once a block.
+//
+// Operands that are not the caller's bf16 values are kept as two bf16 parts (2^-17 of the value),
+// which takes two products against an exact operand and three against another such pair; T is
+// kept as three, since its rounding comes back with every later sub-chunk where keys are alike
+// and strengths are near two (the state then off by 1e-4 instead of 3e-5 after 150 tokens).
+// Sums are fp32.  mma.sync, not tcgen05: the chain's products are 16 x 16 x 64 and smaller and each
+// needs the one before it, which as tcgen05.mma is a round through shared memory, a barrier, a
+// commit and TMEM loads, several hundred cycles, against 21 cycles for a register-to-register
+// mma.sync (8 cycles a warp scheduler, measured).
+#pragma once
+
+#include "gated_delta.h"
+#include "gated_delta_math.cuh"
+#include "warp_mma.cuh"
+
+namespace goldwkv {
+namespace gdr {
+
+using namespace wm;
+
+constexpr int kSub = 16;                    // tokens of a sub-chunk
+constexpr int kSubs = C / kSub;
+constexpr int kWarps = 8;
+constexpr int kTcThreads = 32 * kWarps;
+constexpr uint32_t kTileBytes = C * C * 2;  // 64 rows of 128 bytes
+constexpr int kRow16 = 48;                  // row bytes of a 16 x 16 bf16 tile: no bank conflicts
+constexpr int kTile16 = kSub * kRow16;
+
+// What the preparation hands to the chain for one block.
+struct Prep {
+    uint8_t t[3][kSubs][kTile16];    // T in three parts, [t][s]
+    uint8_t p[2][kSubs][kTile16];    // P in two
+    float g[C];                      // e^L inside the sub-chunk
+    float to_end[C];
+    float beta[C];
+    float g_end[kSubs];
+};
+
+// 16 x 16 tile (rows of kRow16 bytes): both n halves of a B operand from [n][k] rows ...
+__device__ __forceinline__ uint32_t addr16_b(uint32_t tile, int lane) {
+    return tile + (uint32_t)((((lane >> 4) << 3) + (lane & 7)) * kRow16 + ((lane >> 3) & 1) * 16);
+}
+// ... and from [k][n] rows (.trans)
+__device__ __forceinline__ uint32_t addr16_bt(uint32_t tile, int lane) {
+    return tile + (uint32_t)((lane & 15) * kRow16 + (lane >> 4) * 16);
+}
+
+// Rows t0 .. t0 + 63 of a token tensor (row stride `step` values) into a tile by `threads`
+// threads; rows at T or beyond as zeros.
+template <int kThreads>
+__device__ __forceinline__ void copy_block(uint32_t tile, const __nv_bfloat16* base, size_t step, int t0,
+                                           int T, int tid) {
+#pragma unroll
+    for (int i = 0; i < C * 8 / kThreads; ++i) {
+        const int row = (tid >> 3) + i * (kThreads / 8), chunk = tid & 7;
+        const bool in = t0 + row < T;
+        cp_async16(tile + sw_off(row, chunk), base + (in ? (size_t)(t0 + row) * step : 0) + chunk * 8, in);
+    }
+}
+
+// Decay rate and write strength of a lane's token (lanes 16-31 as lanes 0-15); tokens at T or
+// beyond neither decay nor write.
+struct Gate {
+    float rate, beta;
+};
+__device__ __forceinline__ Gate load_gate(const __nv_bfloat16* omega, const __nv_bfloat16* beta, int stride, int t, int T) {
+    Gate g{0.f, 0.f};
+    if (t < T) {
+        g.rate = decay_rate(to_f32(omega[(size_t)t * stride]));
+        g.beta = to_f32(beta[(size_t)t * stride]);
+    }
+    return g;
+}
+
+// One warp prepares sub-chunk j of a block.  at: 16 x 20 floats of the warp's own.
+template <bool kP>
+__device__ __forceinline__ void prepare_sub(Prep& out, float* at, uint32_t kt, uint32_t qt, int j, Gate gate,
+                                            float scale, int lane) {
+    const int r = lane >> 2, c = 2 * (lane & 3);
+    // running sums of log2 w in 64 bits, kept as two floats: a difference then carries its own
+    // rounding only, not that of a sum that one strong decay has made large
+    double l = -1.4426950408889634 * (double)gate.rate;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+        const double x = __shfl_up_sync(0xffffffffu, l, o, 16);
+        if ((lane & 15) >= o) l += x;
+    }
+    const double total = __shfl_sync(0xffffffffu, l, 15, 16);
+    const float hi = (float)l, lo = (float)(l - (double)hi);
+    if (lane < 16) {
+        out.g[kSub * j + lane] = exp2f(hi);
+        out.to_end[kSub * j + lane] = exp2f((float)(total - l));
+        out.beta[kSub * j + lane] = gate.beta;
+        if (lane == 15) out.g_end[j] = exp2f(hi);
+    }
+    float kk[2][4], qk[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        clear(kk[n]);
+        clear(qk[n]);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        uint32_t a[4], b[4];
+        ldsm4(b, addr_b(kt, kSub * j, 2 * s, lane));
+        ldsm4(a, addr_a(kt, kSub * j, 2 * s, lane));
+        mma(kk[0], a, b[0], b[1]);
+        mma(kk[1], a, b[2], b[3]);
+        if (kP) {
+            ldsm4(a, addr_a(qt, kSub * j, 2 * s, lane));
+            mma(qk[0], a, b[0], b[1]);
+            mma(qk[1], a, b[2], b[3]);
+        }
+    }
+    const float h0 = __shfl_sync(0xffffffffu, hi, r), l0 = __shfl_sync(0xffffffffu, lo, r);
+    const float h1 = __shfl_sync(0xffffffffu, hi, r + 8), l1 = __shfl_sync(0xffffffffu, lo, r + 8);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int u = 8 * n + c + e;
+            const float hu = __shfl_sync(0xffffffffu, hi, u), lu = __shfl_sync(0xffffffffu, lo, u);
+            const float bu = __shfl_sync(0xffffffffu, gate.beta, u);
+            // above the diagonal the difference is positive and may overflow: not taken there
+            const float d0 = r >= u ? exp2f((h0 - hu) + (l0 - lu)) : 0.f;
+            const float d1 = r + 8 >= u ? exp2f((h1 - hu) + (l1 - lu)) : 0.f;
+            at[u * 20 + r] = r > u ? kk[n][e] * d0 * bu : 0.f;        // (M b)^T
+            at[u * 20 + r + 8] = r + 8 > u ? kk[n][2 + e] * d1 * bu : 0.f;
+            if (kP) {
+                qk[n][e] = r >= u ? scale * qk[n][e] * d0 : 0.f;
+                qk[n][2 + e] = r + 8 >= u ? scale * qk[n][2 + e] * d1 : 0.f;
+            }
+        }
+    __syncwarp();
+    // (I + M b)^-1 by substitution, a lane a column.  Not a power series: every entry of the
+    // inverse stays bounded where keys are alike, while the powers of M b grow and cancel.
+    float x[kSub];
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) x[i] = i == (lane & 15) ? 1.f : 0.f;
+#pragma unroll
+    for (int s = 0; s < kSub - 1; ++s)
+#pragma unroll
+        for (int i = (s + 1) & ~3; i < kSub; i += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(at + s * 20 + i);   // zero up to i == s
+            x[i] = fmaf(-m.x, x[s], x[i]);
+            x[i + 1] = fmaf(-m.y, x[s], x[i + 1]);
+            x[i + 2] = fmaf(-m.z, x[s], x[i + 2]);
+            x[i + 3] = fmaf(-m.w, x[s], x[i + 3]);
+        }
+    // lanes 0-15 store the first part of their column and the third, lanes 16-31 the second
+    uint8_t* dst = out.t[lane >> 4][j] + 2 * (lane & 15);
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(x[i]);
+        const float rest = x[i] - __bfloat162float(h);
+        const __nv_bfloat16 m = __float2bfloat16_rn(rest);
+        *reinterpret_cast<__nv_bfloat16*>(dst + i * kRow16) = lane < 16 ? h : m;
+        if (lane < 16)
+            *reinterpret_cast<__nv_bfloat16*>(out.t[2][j] + 2 * lane + i * kRow16) =
+                __float2bfloat16_rn(rest - __bfloat162float(m));
+    }
+    if (kP) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t a, b;
+                split2(make_float2(qk[n][2 * h], qk[n][2 * h + 1]), a, b);
+                const int o = (r + 8 * h) * kRow16 + (8 * n + c) * 2;
+                *reinterpret_cast<uint32_t*>(out.p[0][j] + o) = a;
+                *reinterpret_cast<uint32_t*>(out.p[1][j] + o) = b;
+            }
+    }
+    __syncwarp();
+}
+
+// E^T = F^T T^T (kTrans: F^T T) for a chain warp: F^T as an A fragment in two parts, `t` the
+// sub-chunk's tile of T's first part.  The smallest terms first.
+template <bool kTrans = false>
+__device__ __forceinline__ void times_t(float (&e)[2][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4],
+                                        uint32_t t, int lane) {
+    uint32_t b0[4], b1[4], b2[4];
+    const uint32_t at = kTrans ? addr16_bt(t, lane) : addr16_b(t, lane);
+    if (kTrans) {
+        ldsm4t(b0, at);
+        ldsm4t(b1, at + kSubs * kTile16);
+        ldsm4t(b2, at + 2 * kSubs * kTile16);
+    } else {
+        ldsm4(b0, at);
+        ldsm4(b1, at + kSubs * kTile16);
+        ldsm4(b2, at + 2 * kSubs * kTile16);
+    }
+    float f[2][4];   // two chains of sums, half as long
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        clear(e[i]);
+        clear(f[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) mma(f[i], lo, b1[2 * i], b1[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) mma(e[i], hi, b2[2 * i], b2[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) mma(f[i], lo, b0[2 * i], b0[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) mma(e[i], hi, b1[2 * i], b1[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) mma(f[i], hi, b0[2 * i], b0[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) e[i][m] += f[i][m];
+}
+
+}  // namespace gdr
+}  // namespace goldwkv

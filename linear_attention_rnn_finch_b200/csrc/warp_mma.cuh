@@ -1,0 +1,82 @@
+// Device helpers of the register-resident matrix products (mma.sync m16n8k16, bf16 operands,
+// fp32 sums): fragment loads from 128-byte-row tiles, hi/lo splitting, asynchronous copies.
+//
+// Fragments of a lane, g = lane / 4, c = 2 (lane % 4):
+//   accumulator  m16 x n8:  [0,1] = row g, columns c, c+1;  [2,3] = row g + 8
+//   A            m16 x k16: [0] = row g, k c, c+1;  [1] = row g + 8;  [2], [3] = k + 8
+//   B            k16 x n8:  [0] = k c, c+1, column g;  [1] = k + 8
+// Two accumulators side by side (columns 0-7, 8-15), packed to bf16, are an A fragment: a
+// result whose row index stays a row and whose column index is contracted next never leaves
+// the registers.
+#pragma once
+
+#include <stdint.h>
+
+#include "chunk_tiles.cuh"
+
+namespace goldwkv {
+namespace wm {
+
+using tiles::pack2;
+using tiles::split2;
+using tiles::sw_off;
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
+                 :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// d += a b
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void clear(float (&d)[4]) { d[0] = d[1] = d[2] = d[3] = 0.f; }
+
+// Two adjacent accumulators as an A fragment in two bf16 parts: x = hi + lo within 2^-17 |x|.
+__device__ __forceinline__ void split_a(uint32_t (&hi)[4], uint32_t (&lo)[4], const float (&x)[4], const float (&y)[4]) {
+    split2(make_float2(x[0], x[1]), hi[0], lo[0]);
+    split2(make_float2(x[2], x[3]), hi[1], lo[1]);
+    split2(make_float2(y[0], y[1]), hi[2], lo[2]);
+    split2(make_float2(y[2], y[3]), hi[3], lo[3]);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
+// ldmatrix addresses.  Tiles have 128-byte rows whose 16-byte chunks are XORed with the row
+// (sw_off); `row` is the first of 16 rows, `chunk` the first of two adjacent 16-byte chunks.
+// A operand [m][k], rows m:            registers = a[0..3]
+__device__ __forceinline__ uint32_t addr_a(uint32_t tile, int row, int chunk, int lane) {
+    return tile + sw_off(row + (lane & 15), chunk + (lane >> 4));
+}
+// B operand from [n][k] rows, 16 n:    registers = b0, b1 of the first 8 n, then of the next 8
+__device__ __forceinline__ uint32_t addr_b(uint32_t tile, int row, int chunk, int lane) {
+    return tile + sw_off(row + ((lane >> 4) << 3) + (lane & 7), chunk + ((lane >> 3) & 1));
+}
+// B operand from [k][n] rows (.trans): 16 k rows, 16 n columns: b0, b1 of n 0-7, then of n 8-15
+__device__ __forceinline__ uint32_t addr_bt(uint32_t tile, int row, int chunk, int lane) {
+    return tile + sw_off(row + (lane & 15), chunk + (lane >> 4));
+}
+// Accumulator layout of the transpose of a [n][m] bf16 tile (.trans): registers = (m 0-7, n 0-7),
+// (m 8-15, n 0-7), (m 0-7, n 8-15), (m 8-15, n 8-15); also where .trans stores put it back
+__device__ __forceinline__ uint32_t addr_ct(uint32_t tile, int row, int chunk, int lane) {
+    return tile + sw_off(row + ((lane >> 4) << 3) + (lane & 7), chunk + ((lane >> 3) & 1));
+}
+
+}  // namespace wm
+}  // namespace goldwkv
