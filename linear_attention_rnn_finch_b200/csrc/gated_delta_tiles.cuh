@@ -12,7 +12,8 @@
 // longer chain of dependent products is hidden by the other CTA of the SM.
 //
 // Four warps (the chain) own 16 value columns each and keep S^T in registers as accumulators
-// (rows value columns, columns key channels).  Everything transposed (F^T = V^T - g S^T K^T,
+// (rows value columns, columns key channels; two warps of 32 columns issue less in all, but
+// leave schedulers idle: B8 T4096 H32 423 us against 289).  Everything transposed (F^T = V^T - g S^T K^T,
 // E^T = F^T T^T, ...) each result has the layout of the next product's A operand, so a block
 // passes through them without shared memory or barriers between its products.  Four more warps
 // (the preparation) work one block ahead: they issue the copies of the block after it, and
@@ -39,8 +40,9 @@ using namespace wm;
 
 constexpr int kSub = 16;                    // tokens of a sub-chunk
 constexpr int kSubs = C / kSub;
-constexpr int kWarps = 8;
-constexpr int kTcThreads = 32 * kWarps;
+constexpr int kChainWarps = 4;
+constexpr int kPrepThreads = 128;
+constexpr int kTcThreads = 256;             // chain warps, then as many of preparation
 constexpr uint32_t kTileBytes = C * C * 2;  // 64 rows of 128 bytes
 constexpr int kRow16 = 48;                  // row bytes of a 16 x 16 bf16 tile: no bank conflicts
 constexpr int kTile16 = kSub * kRow16;
@@ -80,14 +82,14 @@ __device__ __forceinline__ void copy_block(uint32_t tile, const __nv_bfloat16* b
 // Decay rate and write strength of a lane's token (lanes 16-31 as lanes 0-15); tokens at T or
 // beyond neither decay nor write.
 struct Gate {
-    float rate, beta;
+    __nv_bfloat16 omega, beta;   // as stored: converted at their use, a block later
+    bool in;
 };
 __device__ __forceinline__ Gate load_gate(const __nv_bfloat16* omega, const __nv_bfloat16* beta, int stride, int t, int T) {
-    Gate g{0.f, 0.f};
-    if (t < T) {
-        g.rate = decay_rate(to_f32(omega[(size_t)t * stride]));
-        g.beta = to_f32(beta[(size_t)t * stride]);
-    }
+    Gate g;
+    g.in = t < T;
+    g.omega = g.in ? omega[(size_t)t * stride] : __nv_bfloat16(0.f);
+    g.beta = g.in ? beta[(size_t)t * stride] : __nv_bfloat16(0.f);
     return g;
 }
 
@@ -96,9 +98,11 @@ template <bool kP>
 __device__ __forceinline__ void prepare_sub(Prep& out, float* at, uint32_t kt, uint32_t qt, int j, Gate gate,
                                             float scale, int lane) {
     const int r = lane >> 2, c = 2 * (lane & 3);
+    const uint32_t ka = addr_a(kt, kSub * j, 0, lane), kb = addr_b(kt, kSub * j, 0, lane), qa = ka + (qt - kt);
     // running sums of log2 w in 64 bits, kept as two floats: a difference then carries its own
     // rounding only, not that of a sum that one strong decay has made large
-    double l = -1.4426950408889634 * (double)gate.rate;
+    const float beta = to_f32(gate.beta);
+    double l = gate.in ? -1.4426950408889634 * (double)decay_rate(to_f32(gate.omega)) : 0.0;
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) {
         const double x = __shfl_up_sync(0xffffffffu, l, o, 16);
@@ -109,7 +113,7 @@ __device__ __forceinline__ void prepare_sub(Prep& out, float* at, uint32_t kt, u
     if (lane < 16) {
         out.g[kSub * j + lane] = exp2f(hi);
         out.to_end[kSub * j + lane] = exp2f((float)(total - l));
-        out.beta[kSub * j + lane] = gate.beta;
+        out.beta[kSub * j + lane] = beta;
         if (lane == 15) out.g_end[j] = exp2f(hi);
     }
     float kk[2][4], qk[2][4];
@@ -121,12 +125,12 @@ __device__ __forceinline__ void prepare_sub(Prep& out, float* at, uint32_t kt, u
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         uint32_t a[4], b[4];
-        ldsm4(b, addr_b(kt, kSub * j, 2 * s, lane));
-        ldsm4(a, addr_a(kt, kSub * j, 2 * s, lane));
+        ldsm4(b, step(kb, s));
+        ldsm4(a, step(ka, s));
         mma(kk[0], a, b[0], b[1]);
         mma(kk[1], a, b[2], b[3]);
         if (kP) {
-            ldsm4(a, addr_a(qt, kSub * j, 2 * s, lane));
+            ldsm4(a, step(qa, s));
             mma(qk[0], a, b[0], b[1]);
             mma(qk[1], a, b[2], b[3]);
         }
@@ -139,10 +143,10 @@ __device__ __forceinline__ void prepare_sub(Prep& out, float* at, uint32_t kt, u
         for (int e = 0; e < 2; ++e) {
             const int u = 8 * n + c + e;
             const float hu = __shfl_sync(0xffffffffu, hi, u), lu = __shfl_sync(0xffffffffu, lo, u);
-            const float bu = __shfl_sync(0xffffffffu, gate.beta, u);
+            const float bu = __shfl_sync(0xffffffffu, beta, u);
             // above the diagonal the difference is positive and may overflow: not taken there
-            const float d0 = r >= u ? exp2f((h0 - hu) + (l0 - lu)) : 0.f;
-            const float d1 = r + 8 >= u ? exp2f((h1 - hu) + (l1 - lu)) : 0.f;
+            const float d0 = r >= u ? tiles::fast_exp2((h0 - hu) + (l0 - lu)) : 0.f;
+            const float d1 = r + 8 >= u ? tiles::fast_exp2((h1 - hu) + (l1 - lu)) : 0.f;
             at[u * 20 + r] = r > u ? kk[n][e] * d0 * bu : 0.f;        // (M b)^T
             at[u * 20 + r + 8] = r + 8 > u ? kk[n][2 + e] * d1 * bu : 0.f;
             if (kP) {
@@ -193,12 +197,11 @@ __device__ __forceinline__ void prepare_sub(Prep& out, float* at, uint32_t kt, u
     __syncwarp();
 }
 
-// E^T = F^T T^T (kTrans: F^T T) for a chain warp: F^T as an A fragment in two parts, `t` the
-// sub-chunk's tile of T's first part.  The smallest terms first.
+// E^T = F^T T^T (kTrans: F^T T) for a chain warp: F^T as accumulators, `t` the sub-chunk's tile of
+// T's first part.  The smallest terms first, in two chains of sums.
 template <bool kTrans = false>
-__device__ __forceinline__ void times_t(float (&e)[2][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4],
-                                        uint32_t t, int lane) {
-    uint32_t b0[4], b1[4], b2[4];
+__device__ __forceinline__ void times_t(float (&e)[2][4], const float (&x)[2][4], uint32_t t, int lane) {
+    uint32_t b0[4], b1[4], b2[4], hi[4], lo[4];
     const uint32_t at = kTrans ? addr16_bt(t, lane) : addr16_b(t, lane);
     if (kTrans) {
         ldsm4t(b0, at);
@@ -209,26 +212,76 @@ __device__ __forceinline__ void times_t(float (&e)[2][4], const uint32_t (&hi)[4
         ldsm4(b1, at + kSubs * kTile16);
         ldsm4(b2, at + 2 * kSubs * kTile16);
     }
-    float f[2][4];   // two chains of sums, half as long
+    float f[2][4];
+    split_a(hi, lo, x[0], x[1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        clear(e[i]);
-        clear(f[i]);
+        mma0(e[i], hi, b2[2 * i], b2[2 * i + 1]);
+        mma0(f[i], lo, b1[2 * i], b1[2 * i + 1]);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) mma(f[i], lo, b1[2 * i], b1[2 * i + 1]);
+    for (int i = 0; i < 2; ++i) {
+        mma(e[i], hi, b1[2 * i], b1[2 * i + 1]);
+        mma(f[i], lo, b0[2 * i], b0[2 * i + 1]);
+    }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) mma(e[i], hi, b2[2 * i], b2[2 * i + 1]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) mma(f[i], lo, b0[2 * i], b0[2 * i + 1]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) mma(e[i], hi, b1[2 * i], b1[2 * i + 1]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) mma(f[i], hi, b0[2 * i], b0[2 * i + 1]);
+    for (int i = 0; i < 2; ++i) mma(e[i], hi, b0[2 * i], b0[2 * i + 1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) e[i][m] += f[i][m];
+        for (int k = 0; k < 4; ++k) e[i][k] += f[i][k];
+}
+
+// A state-shaped matrix [key][value] fp32 (null: zeros) to and from a chain warp's accumulators:
+// S[i]: value columns 16 cw + r, + 8; keys 8 i + c, c + 1.
+__device__ __forceinline__ void load_state(float (&S)[8][4], const float* src, int cw, int lane) {
+    const int r = lane >> 2, c = 2 * (lane & 3);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            S[i][e] = src ? src[(8 * i + c + (e & 1)) * C + 16 * cw + r + 8 * (e >> 1)] : 0.f;
+}
+__device__ __forceinline__ void store_state(float* dst, const float (&S)[8][4], int cw, int lane) {
+    const int r = lane >> 2, c = 2 * (lane & 3);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[(8 * i + c + (e & 1)) * C + 16 * cw + r + 8 * (e >> 1)] = S[i][e];
+}
+
+// S^T = factor S^T + X^T K: X^T as accumulators; kt: addr_bt of K's 16 rows at chunk 0.
+__device__ __forceinline__ void update_state(float (&S)[8][4], float factor, const float (&x)[2][4], uint32_t kt) {
+    uint32_t hi[4], lo[4];
+    split_a(hi, lo, x[0], x[1]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t kb[4];
+        ldsm4t(kb, step(kt, i));
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[2 * i + u][e] *= factor;
+            mma(S[2 * i + u], lo, kb[2 * u], kb[2 * u + 1]);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) mma(S[2 * i + u], hi, kb[2 * u], kb[2 * u + 1]);
+    }
+}
+
+// A chain warp's 16 tokens x 16 value columns, as transposed accumulators, rounded to bf16 and
+// put to out (token 0, first column of the warp; row stride `step`), tokens at `count` or beyond
+// not written.  tile: kTile16 bytes of the warp's own, through which they are turned.
+__device__ __forceinline__ void store_tokens(__nv_bfloat16* out, size_t step, int count, const float (&y)[2][4],
+                                             uint8_t* tile, int lane) {
+    __syncwarp();
+    stsm4t(ptx::smem_addr(tile) + (uint32_t)((((lane >> 4) << 3) + (lane & 7)) * kRow16 + ((lane >> 3) & 1) * 16),
+           pack2(y[0][0], y[0][1]), pack2(y[0][2], y[0][3]), pack2(y[1][0], y[1][1]), pack2(y[1][2], y[1][3]));
+    __syncwarp();
+    const int t = lane >> 1;
+    if (t < count)
+        *reinterpret_cast<uint4*>(out + (size_t)t * step + 8 * (lane & 1)) =
+            *reinterpret_cast<const uint4*>(tile + t * kRow16 + (lane & 1) * 16);
 }
 
 }  // namespace gdr

@@ -23,11 +23,11 @@ using tiles::sw_off;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 __device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
@@ -35,13 +35,39 @@ __device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t a, uint32_t b, ui
 }
 // d += a b
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// d = a b
+__device__ __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void clear(float (&d)[4]) { d[0] = d[1] = d[2] = d[3] = 0.f; }
+
+// x[0], x[2] *= s.x; x[1], x[3] *= s.y: a factor for each column
+__device__ __forceinline__ void scale_cols(float (&x)[4], float2 s) {
+    const float2 a = __fmul2_rn(make_float2(x[0], x[1]), s), b = __fmul2_rn(make_float2(x[2], x[3]), s);
+    x[0] = a.x;
+    x[1] = a.y;
+    x[2] = b.x;
+    x[3] = b.y;
+}
+// x = v - s x, v as two packed pairs of bf16
+__device__ __forceinline__ void value_minus(float (&x)[4], float2 s, uint32_t v0, uint32_t v1) {
+    const float2 n = make_float2(-s.x, -s.y);
+    const float2 a = __ffma2_rn(make_float2(x[0], x[1]), n, tiles::unpack2(v0));
+    const float2 b = __ffma2_rn(make_float2(x[2], x[3]), n, tiles::unpack2(v1));
+    x[0] = a.x;
+    x[1] = a.y;
+    x[2] = b.x;
+    x[3] = b.y;
+}
 
 // Two adjacent accumulators as an A fragment in two bf16 parts: x = hi + lo within 2^-17 |x|.
 __device__ __forceinline__ void split_a(uint32_t (&hi)[4], uint32_t (&lo)[4], const float (&x)[4], const float (&y)[4]) {
@@ -60,6 +86,8 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_gr
 
 // ldmatrix addresses.  Tiles have 128-byte rows whose 16-byte chunks are XORed with the row
 // (sw_off); `row` is the first of 16 rows, `chunk` the first of two adjacent 16-byte chunks.
+// Tiles lie on 1024-byte boundaries, so that two chunks further (step) is an XOR of the address.
+__device__ __forceinline__ uint32_t step(uint32_t addr, int i) { return addr ^ (uint32_t)(i << 5); }
 // A operand [m][k], rows m:            registers = a[0..3]
 __device__ __forceinline__ uint32_t addr_a(uint32_t tile, int row, int chunk, int lane) {
     return tile + sw_off(row + (lane & 15), chunk + (lane >> 4));
