@@ -45,4 +45,8 @@ size_t gdr_backward_simt_bytes(int B, int T, int H);
 cudaError_t launch_gdr_backward_simt(const GdrIn& in, const float* s_in, const GdrGrads& g,
                                      void* ws, bool bf16, cudaStream_t st);
 
+// Backward on tensor cores, bf16 I/O.  ws: at least gdr_backward_tc_bytes(B, T, H) bytes.
+size_t gdr_backward_tc_bytes(int B, int T, int H);
+cudaError_t launch_gdr_backward_tc(const GdrIn& in, const float* s_in, const GdrGrads& g, void* ws, cudaStream_t st);
+
 }  // namespace goldwkv

@@ -1,0 +1,629 @@
+// Backward of the gated delta rule, bf16 inputs, on tensor cores (sm_100a).  Formulas: the head of
+// gated_delta_backward.cu; division of labour inside a chain: gated_delta_tiles.cuh.
+//
+// Two launches.  The first runs both chains over a head's blocks of 64 tokens, which need nothing
+// of each other, in CTAs of their own:
+//   forward:  S as in the prefill, without outputs; leaves the state entering each block and E;
+//   backward: with G the gradient of a sub-chunk's final state,
+//                 X = P^T dY + to_end K G,   dF = T^T (b X) = dV,
+//                 G- = g_16 G + (scale g Q)^T dY - (g K)^T dF,
+//             transposed like the forward one; leaves dV, each block's G and dF.
+// The second, parallel over blocks, forms dQ, dK, dbeta and domega from those with the 64-token
+// forms of the formulas (E and dF are the same values however tokens are grouped).  A warp owns
+// 16 tokens: products with S and G contract value columns, which the chains keep on different
+// warps.
+//
+// S, G, E and dF pass between the launches as two bf16 parts (2^-17 of the value, what the
+// products take anyway) in the order of operand fragments: the chain turns them in registers
+// (movmatrix) and stores 16 bytes a lane, and they are read back with neither swizzle nor
+// ldmatrix.  64 KB a head and block.
+#include "common.cuh"
+#include "gated_delta.h"
+#include "gated_delta_tiles.cuh"
+
+namespace goldwkv {
+
+namespace {
+
+using namespace gdr;
+using bf16 = __nv_bfloat16;
+
+constexpr int kStages = 3;
+constexpr size_t kPart = kTileBytes;        // one part of a 64 x 64 matrix
+constexpr size_t kMat = 2 * kPart;          // both
+constexpr size_t kBlockBytes = 4 * kMat;    // S, E, G, dF of a block
+
+struct Args {
+    GdrIn in;
+    GdrGrads g;
+    const float* s_in;
+    uint8_t* ws;     // [head][block][S, E, G, dF]
+    int blocks;
+};
+
+__device__ __forceinline__ uint32_t turn(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// A chain warp's state as the B operand [value][key] of 16 value columns: a quad holds both
+// halves of k for two adjacent key tiles.
+__device__ __forceinline__ void put_state(uint8_t* dst, const float (&S)[8][4], int warp, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t hi[4], lo[4];
+        split_a(hi, lo, S[2 * i], S[2 * i + 1]);
+        uint8_t* at = dst + ((warp * 4 + i) * 32 + lane) * 16;
+        *reinterpret_cast<uint4*>(at) = make_uint4(turn(hi[0]), turn(hi[1]), turn(hi[2]), turn(hi[3]));
+        *reinterpret_cast<uint4*>(at + kPart) = make_uint4(turn(lo[0]), turn(lo[1]), turn(lo[2]), turn(lo[3]));
+    }
+}
+// A sub-chunk's 16 tokens x 16 value columns as an A operand [token][value] (and, its registers
+// taken as 0, 2 and 1, 3, the B operand of the two token tiles).
+__device__ __forceinline__ void put_rows(uint8_t* dst, const float (&e)[2][4], int j, int warp, int lane) {
+    uint32_t hi[4], lo[4];
+    split_a(hi, lo, e[0], e[1]);
+    uint8_t* at = dst + ((j * 4 + warp) * 32 + lane) * 16;
+    *reinterpret_cast<uint4*>(at) = make_uint4(turn(hi[0]), turn(hi[2]), turn(hi[1]), turn(hi[3]));
+    *reinterpret_cast<uint4*>(at + kPart) = make_uint4(turn(lo[0]), turn(lo[2]), turn(lo[1]), turn(lo[3]));
+}
+
+// ------------------------------------------------------------------ the chains
+struct ChainSmem {
+    uint8_t k[kStages][kTileBytes];
+    uint8_t x[kStages][kTileBytes];   // V, or dY
+    uint8_t q[kStages][kTileBytes];   // backward chain
+    Prep prep[2];
+    float at[kChainWarps][kSub * 20];
+    uint8_t y[kChainWarps][kTile16];
+};
+
+template <bool kBack>
+__device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh) {
+    const int H = p.in.H, HK = p.in.HK, T = p.in.T, b = bh / H, h = bh - b * H, hk = h / (H / HK);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, blocks = p.blocks;
+    const size_t ko = ((size_t)b * T * HK + hk) * C, vo = ((size_t)b * T * H + h) * C, go = (size_t)b * T * H + h;
+    const bf16 *q = (const bf16*)p.in.q + ko, *k = (const bf16*)p.in.k + ko;
+    const bf16* x = (const bf16*)(kBack ? p.g.dy : p.in.v) + vo;
+    const uint32_t sk = ptx::smem_addr(s.k), sx = ptx::smem_addr(s.x), sq = ptx::smem_addr(s.q);
+    // the m-th block walked
+    auto block = [&](int m) { return kBack ? blocks - 1 - m : m; };
+
+    if (warp >= kChainWarps) {   // ---- preparation
+        const int w = warp - kChainWarps, pt = tid - kPrepThreads;
+        const bf16 *omega = (const bf16*)p.in.omega + go, *beta = (const bf16*)p.in.beta + go;
+        auto copy = [&](int m) {
+            const uint32_t o = (uint32_t)(m % kStages) * kTileBytes;
+            const int t0 = block(m) * C;
+            copy_block<kPrepThreads>(sk + o, k, (size_t)HK * C, t0, T, pt);
+            copy_block<kPrepThreads>(sx + o, x, (size_t)H * C, t0, T, pt);
+            if (kBack) copy_block<kPrepThreads>(sq + o, q, (size_t)HK * C, t0, T, pt);
+            cp_async_commit();
+        };
+        auto gate_of = [&](int m) {
+            return load_gate(omega, beta, H, m < blocks ? block(m) * C + kSub * w + (lane & 15) : T, T);
+        };
+        copy(0);
+        Gate gate = gate_of(0);
+        cp_async_wait<0>();
+        __syncthreads();
+        for (int m = -1; m < blocks; ++m) {
+            if (m + 2 < blocks) copy(m + 2);
+            if (m + 1 < blocks) {
+                const uint32_t o = (uint32_t)((m + 1) % kStages) * kTileBytes;
+                const Gate next = gate_of(m + 2);
+                prepare_sub<kBack>(s.prep[(m + 1) & 1], s.at[w], sk + o, sq + o, w, gate, p.in.scale, lane);
+                gate = next;
+            }
+            cp_async_wait<0>();
+            __syncthreads();
+        }
+        return;
+    }
+
+    const int c = 2 * (lane & 3);
+    float S[8][4];
+    const float* first = kBack ? p.g.ds_out : p.s_in;
+    load_state(S, first ? first + (size_t)bh * C * C : nullptr, warp, lane);
+    bf16* dv = (bf16*)p.g.dv + vo + 16 * warp;
+    uint8_t* ws = p.ws + (size_t)bh * blocks * kBlockBytes + (kBack ? 2 * kMat : 0);
+    const uint32_t ab = addr_b(0, 0, 0, lane), abt = addr_bt(0, 0, 0, lane), act = addr_ct(0, 0, 2 * warp, lane);
+    __syncthreads();
+    __syncthreads();   // the preparation's first turn
+    for (int m = 0; m < blocks; ++m) {
+        const uint32_t o = (uint32_t)(m % kStages) * kTileBytes;
+        const int t0 = block(m) * C;
+        const Prep& pr = s.prep[m & 1];
+        const uint32_t pt = ptx::smem_addr(pr.t), pp = ptx::smem_addr(pr.p);
+        uint8_t* wb = ws + (size_t)block(m) * kBlockBytes;
+        put_state(wb, S, warp, lane);
+#pragma unroll 1
+        for (int i0 = 0; i0 < kSubs; ++i0) {
+            const int j = kBack ? kSubs - 1 - i0 : i0, row = kSub * j;
+            const uint32_t kt = sk + o + row * 128;
+            float f[2][4], e[2][4];   // S^T K^T (or G^T K^T)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t hi[4], lo[4], kb[4];
+                ldsm4(kb, step(kt + ab, i));
+                split_a(hi, lo, S[2 * i], S[2 * i + 1]);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {   // hi and lo parts in chains of their own
+                    if (i == 0) {
+                        mma0(f[u], hi, kb[2 * u], kb[2 * u + 1]);
+                        mma0(e[u], lo, kb[2 * u], kb[2 * u + 1]);
+                    } else {
+                        mma(f[u], hi, kb[2 * u], kb[2 * u + 1]);
+                        mma(e[u], lo, kb[2 * u], kb[2 * u + 1]);
+                    }
+                }
+            }
+            uint32_t xv[4];   // V^T or dY^T, as the A operand [value][token]
+            ldsm4t(xv, sx + o + row * 128 + act);
+            float2 g[2], bt[2], te[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                g[u] = *reinterpret_cast<const float2*>(&pr.g[row + 8 * u + c]);
+                bt[u] = *reinterpret_cast<const float2*>(&pr.beta[row + 8 * u + c]);
+                te[u] = *reinterpret_cast<const float2*>(&pr.to_end[row + 8 * u + c]);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) f[u][n] += e[u][n];
+            }
+            if (!kBack) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) value_minus(f[u], g[u], xv[2 * u], xv[2 * u + 1]);
+                times_t(e, f, pt + j * kTile16, lane);
+                put_rows(wb + kMat, e, j, warp, lane);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) scale_cols(e[u], make_float2(bt[u].x * te[u].x, bt[u].y * te[u].y));
+                update_state(S, pr.g_end[j], e, kt + abt);
+            } else {
+                // X^T = to_end G^T K^T + dY^T P
+                uint32_t p0[4], p1[4];
+                ldsm4t(p0, addr16_bt(pp + j * kTile16, lane));
+                ldsm4t(p1, addr16_bt(pp + (kSubs + j) * kTile16, lane));
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    scale_cols(f[u], te[u]);
+                    mma(f[u], xv, p1[2 * u], p1[2 * u + 1]);
+                    mma(f[u], xv, p0[2 * u], p0[2 * u + 1]);
+                    scale_cols(f[u], bt[u]);
+                }
+                times_t<true>(e, f, pt + j * kTile16, lane);
+                store_tokens(dv + (size_t)(t0 + row) * H * C, (size_t)H * C, T - t0 - row, e, s.y[warp], lane);
+                put_rows(wb + kMat, e, j, warp, lane);
+                // G^T = g_16 G^T + (scale g dY)^T Q - (g dF)^T K
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float2 y0 = tiles::unpack2(xv[2 * u]), y1 = tiles::unpack2(xv[2 * u + 1]);
+                    f[u][0] = y0.x;
+                    f[u][1] = y0.y;
+                    f[u][2] = y1.x;
+                    f[u][3] = y1.y;
+                    scale_cols(f[u], make_float2(p.in.scale * g[u].x, p.in.scale * g[u].y));
+                    scale_cols(e[u], make_float2(-g[u].x, -g[u].y));
+                }
+                update_state(S, pr.g_end[j], f, kt + abt + (sq - sk));
+                update_state(S, 1.f, e, kt + abt);
+            }
+        }
+        __syncthreads();
+    }
+    if (kBack && p.g.ds_in) store_state(p.g.ds_in + (size_t)bh * C * C, S, warp, lane);
+}
+
+__global__ void __launch_bounds__(kTcThreads, 2)
+gated_delta_bwd_chains_kernel(const __grid_constant__ Args p) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    ChainSmem& s = tiles::smem_aligned<ChainSmem>(raw);
+    // the longer chain first
+    const int heads = p.in.B * p.in.H;
+    if ((int)blockIdx.x < heads) chain<true>(s, p, blockIdx.x);
+    else chain<false>(s, p, blockIdx.x - heads);
+}
+
+// ------------------------------------------------------------------ dQ, dK, dbeta, domega
+// A warp owns tokens 16 w .. 16 w + 15 as rows.  Per value head: products over value columns with
+// S and G, then the 64 x 64 lower triangles, whose rows a warp contracts from its registers and
+// whose columns (dP^T Q, dM^T K) it reads back from shared memory, over S and G's place.  Warp w
+// has w + 1 row and 4 - w column tiles: the same work for each.
+struct OutSmem {
+    uint8_t q[kTileBytes], k[kTileBytes], dy[kTileBytes];
+    union {
+        struct {
+            uint8_t s[kMat], g[kMat];
+        };
+        struct {
+            uint8_t dp[2][kTileBytes], dm[2][kTileBytes];   // [t][s], hi and lo parts
+        };
+    };
+    uint8_t e[kMat];
+    Gates gates;
+    float cols[4][C];     // column sums of P dY E - M dF E over each warp's rows
+    float reads[C], kte[C];
+    float gs[4];
+    float diag[4][kSub * 17];
+};
+
+__device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void get(uint32_t (&r)[4], const uint8_t* p) {
+    const uint4 x = lds128(p);
+    r[0] = x.x;
+    r[1] = x.y;
+    r[2] = x.z;
+    r[3] = x.w;
+}
+
+__global__ void __launch_bounds__(128, 2)
+gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    OutSmem& s = tiles::smem_aligned<OutSmem>(raw);
+    const int n = blockIdx.x % p.blocks, bk = blockIdx.x / p.blocks;
+    const int H = p.in.H, HK = p.in.HK, T = p.in.T, b = bk / HK, hk = bk - b * HK, per = H / HK;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, r = lane >> 2, c = 2 * (lane & 3);
+    const int t0 = n * C, row = kSub * w;
+    const size_t ko = ((size_t)b * T * HK + hk) * C;
+    const uint32_t sq = ptx::smem_addr(s.q), sk = ptx::smem_addr(s.k), sy = ptx::smem_addr(s.dy);
+    const uint32_t sp = ptx::smem_addr(s.dp), sm = ptx::smem_addr(s.dm);
+    copy_block<128>(sq, (const bf16*)p.in.q + ko, (size_t)HK * C, t0, T, tid);
+    copy_block<128>(sk, (const bf16*)p.in.k + ko, (size_t)HK * C, t0, T, tid);
+    float dq[8][4], dk[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        clear(dq[i]);
+        clear(dk[i]);
+    }
+    for (int h = hk * per; h < (hk + 1) * per; ++h) {
+        const size_t bh = (size_t)b * H + h;
+        const uint8_t* wb = p.ws + (bh * p.blocks + n) * kBlockBytes;
+        copy_block<128>(sy, (const bf16*)p.g.dy + ((size_t)b * T * H + h) * C, (size_t)H * C, t0, T, tid);
+#pragma unroll
+        for (int i = 0; i < (int)(kMat / 16 / 128); ++i) {
+            const int o = (i * 128 + tid) * 16;
+            cp_async16(ptx::smem_addr(s.s) + o, wb + o, true);
+            cp_async16(ptx::smem_addr(s.g) + o, wb + 2 * kMat + o, true);
+            cp_async16(ptx::smem_addr(s.e) + o, wb + kMat + o, true);
+        }
+        cp_async_commit();
+        // this warp's rows of dF, in two parts
+        uint32_t fh[4][4], fl[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint8_t* at = wb + 3 * kMat + ((w * 4 + i) * 32 + lane) * 16;
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
+            const uint4 y = __ldg(reinterpret_cast<const uint4*>(at + kPart));
+            fh[i][0] = x.x; fh[i][1] = x.y; fh[i][2] = x.z; fh[i][3] = x.w;
+            fl[i][0] = y.x; fl[i][1] = y.y; fl[i][2] = y.z; fl[i][3] = y.w;
+        }
+        load_gates(s.gates, (const bf16*)p.in.omega, (const bf16*)p.in.beta, (size_t)b * T * H + h, H, t0, T);
+        cp_async_wait<0>();
+        __syncthreads();
+
+        // ---- with the states: dQ += scale g (dY S^T), dK += b to_end (E G^T) - g (dF S^T)
+        const float g0 = s.gates.g[row + r], g1 = s.gates.g[row + r + 8];
+        const float e0 = s.gates.to_end[row + r], e1 = s.gates.to_end[row + r + 8];
+        const float b0 = s.gates.beta[row + r], b1 = s.gates.beta[row + r + 8];
+        float rd0 = 0.f, rd1 = 0.f, ke0 = 0.f, ke1 = 0.f;
+        uint32_t ya[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ldsm4(ya[i], step(addr_a(sy, row, 0, lane), i));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // two key tiles
+            float a[2][4], f[2][4], eg[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                clear(a[u]);
+                clear(f[u]);
+                clear(eg[u]);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {   // 16 value columns
+                uint32_t sh[4], sl[4], gh[4], gl[4], eh[4], el[4];
+                const int o = ((m * 4 + i) * 32 + lane) * 16;
+                get(sh, s.s + o);
+                get(sl, s.s + kPart + o);
+                get(gh, s.g + o);
+                get(gl, s.g + kPart + o);
+                get(eh, s.e + ((w * 4 + m) * 32 + lane) * 16);
+                get(el, s.e + kPart + ((w * 4 + m) * 32 + lane) * 16);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    mma(a[u], ya[m], sl[2 * u], sl[2 * u + 1]);
+                    mma(f[u], fl[m], sh[2 * u], sh[2 * u + 1]);
+                    mma(eg[u], el, gh[2 * u], gh[2 * u + 1]);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    mma(a[u], ya[m], sh[2 * u], sh[2 * u + 1]);
+                    mma(f[u], fh[m], sl[2 * u], sl[2 * u + 1]);
+                    mma(eg[u], eh, gl[2 * u], gl[2 * u + 1]);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    mma(f[u], fh[m], sh[2 * u], sh[2 * u + 1]);
+                    mma(eg[u], eh, gh[2 * u], gh[2 * u + 1]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int kt = 2 * i + u;
+                const float2 q0 = tiles::unpack2(tiles::lds32(s.q, sw_off(row + r, kt) + 2 * c));
+                const float2 q1 = tiles::unpack2(tiles::lds32(s.q, sw_off(row + r + 8, kt) + 2 * c));
+                const float2 k0 = tiles::unpack2(tiles::lds32(s.k, sw_off(row + r, kt) + 2 * c));
+                const float2 k1 = tiles::unpack2(tiles::lds32(s.k, sw_off(row + r + 8, kt) + 2 * c));
+                const float qv[4] = {q0.x, q0.y, q1.x, q1.y}, kv[4] = {k0.x, k0.y, k1.x, k1.y};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float g = x < 2 ? g0 : g1, te = x < 2 ? e0 : e1, bt = x < 2 ? b0 : b1;
+                    const float av = p.in.scale * g * a[u][x], fv = g * f[u][x], ev = te * eg[u][x];
+                    dq[kt][x] += av;
+                    dk[kt][x] += fmaf(bt, ev, -fv);
+                    const float rd = fmaf(qv[x], av, -kv[x] * fv), ke = kv[x] * ev;
+                    if (x < 2) {
+                        rd0 += rd;
+                        ke0 += ke;
+                    } else {
+                        rd1 += rd;
+                        ke1 += ke;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            rd0 += __shfl_xor_sync(0xffffffffu, rd0, o);
+            rd1 += __shfl_xor_sync(0xffffffffu, rd1, o);
+            ke0 += __shfl_xor_sync(0xffffffffu, ke0, o);
+            ke1 += __shfl_xor_sync(0xffffffffu, ke1, o);
+        }
+        if ((lane & 3) == 0) {
+            s.reads[row + r] = rd0;
+            s.reads[row + r + 8] = rd1;
+            s.kte[row + r] = ke0;
+            s.kte[row + r + 8] = ke1;
+        }
+        // <G, S>, 16 value columns a warp
+        float gs = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t sh[4], sl[4], gh[4], gl[4];
+            const int o = ((w * 4 + i) * 32 + lane) * 16;
+            get(sh, s.s + o);
+            get(sl, s.s + kPart + o);
+            get(gh, s.g + o);
+            get(gl, s.g + kPart + o);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float2 a = tiles::unpack2(sh[x]), al = tiles::unpack2(sl[x]);
+                const float2 d = tiles::unpack2(gh[x]), dl = tiles::unpack2(gl[x]);
+                gs = fmaf(a.x + al.x, d.x + dl.x, gs);
+                gs = fmaf(a.y + al.y, d.y + dl.y, gs);
+            }
+        }
+        gs = warp_sum(gs);
+        if (lane == 0) s.gs[w] = gs;
+        __syncthreads();   // S and G are read: their place takes dP and dM
+
+        // ---- the triangles, a tile of 16 x 16 at a time
+        uint32_t qa[4][4], ka[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ldsm4(qa[i], step(addr_a(sq, row, 0, lane), i));
+            ldsm4(ka[i], step(addr_a(sk, row, 0, lane), i));
+        }
+        const float h0 = s.gates.hi[row + r], l0 = s.gates.lo[row + r];
+        const float h1 = s.gates.hi[row + r + 8], l1 = s.gates.lo[row + r + 8];
+        float rows0 = 0.f, rows1 = 0.f;   // sums of W over the tiles left of the diagonal
+        for (int v = 0; v <= w; ++v) {
+            float qk[2][4], kk[2][4], ye[2][4], fe[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                clear(qk[u]);
+                clear(kk[u]);
+                clear(ye[u]);
+                clear(fe[u]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t kb[4], eh[4], el[4];
+                ldsm4(kb, step(addr_b(sk, kSub * v, 0, lane), i));
+                get(eh, s.e + ((v * 4 + i) * 32 + lane) * 16);
+                get(el, s.e + kPart + ((v * 4 + i) * 32 + lane) * 16);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {   // E's rows as B: registers 0, 2 and 1, 3
+                    mma(qk[u], qa[i], kb[2 * u], kb[2 * u + 1]);
+                    mma(kk[u], ka[i], kb[2 * u], kb[2 * u + 1]);
+                    mma(ye[u], ya[i], el[u], el[u + 2]);
+                    mma(fe[u], fl[i], eh[u], eh[u + 2]);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    mma(ye[u], ya[i], eh[u], eh[u + 2]);
+                    mma(fe[u], fh[i], el[u], el[u + 2]);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) mma(fe[u], fh[i], eh[u], eh[u + 2]);
+            }
+            float cs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int cl = 8 * u + c + (x & 1), sc = kSub * v + cl, rl = r + 8 * (x >> 1);
+                    const bool on = v < w || rl >= cl, below = v < w || rl > cl;
+                    const float hh = x < 2 ? h0 : h1, ll = x < 2 ? l0 : l1;
+                    const float d = on ? tiles::fast_exp2((hh - s.gates.hi[sc]) + (ll - s.gates.lo[sc])) : 0.f;
+                    const float bs = s.gates.beta[sc], ds = p.in.scale * d;
+                    const float y = on ? ye[u][x] : 0.f, f = below ? fe[u][x] : 0.f;
+                    const float sum = ds * qk[u][x] * y - d * kk[u][x] * f;
+                    cs[2 * u + (x & 1)] += sum;
+                    const float wt = below ? bs * sum : 0.f;
+                    if (v < w) {
+                        if (x < 2) rows0 += wt;
+                        else rows1 += wt;
+                    } else {
+                        s.diag[w][rl * 17 + cl] = wt;
+                    }
+                    ye[u][x] = ds * bs * y;      // dP
+                    fe[u][x] = -d * bs * f;      // dM
+                }
+            // column sums over the warp's 16 rows
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) cs[x] += __shfl_xor_sync(0xffffffffu, cs[x], o);
+            if (lane < 4) {
+                s.cols[w][kSub * v + c] = cs[0];
+                s.cols[w][kSub * v + c + 1] = cs[1];
+                s.cols[w][kSub * v + 8 + c] = cs[2];
+                s.cols[w][kSub * v + 8 + c + 1] = cs[3];
+            }
+            uint32_t ph[4], pl[4], mh[4], ml[4];
+            split_a(ph, pl, ye[0], ye[1]);
+            split_a(mh, ml, fe[0], fe[1]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t o = sw_off(row + r + 8 * (x & 1), 2 * v + (x >> 1)) + 2 * c;
+                tiles::sts32(s.dp[0], o, ph[x]);
+                tiles::sts32(s.dp[1], o, pl[x]);
+                tiles::sts32(s.dm[0], o, mh[x]);
+                tiles::sts32(s.dm[1], o, ml[x]);
+            }
+            // dQ += dP K, dK += dM K
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t kb[4];
+                ldsm4t(kb, step(addr_bt(sk, kSub * v, 0, lane), i));
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    mma(dq[2 * i + u], pl, kb[2 * u], kb[2 * u + 1]);
+                    mma(dk[2 * i + u], ml, kb[2 * u], kb[2 * u + 1]);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    mma(dq[2 * i + u], ph, kb[2 * u], kb[2 * u + 1]);
+                    mma(dk[2 * i + u], mh, kb[2 * u], kb[2 * u + 1]);
+                }
+            }
+        }
+        rows0 += __shfl_xor_sync(0xffffffffu, rows0, 1);
+        rows1 += __shfl_xor_sync(0xffffffffu, rows1, 1);
+        rows0 += __shfl_xor_sync(0xffffffffu, rows0, 2);
+        rows1 += __shfl_xor_sync(0xffffffffu, rows1, 2);
+        __syncthreads();
+        // ---- their columns: dK += dP^T Q + dM^T K
+        for (int v = w; v < 4; ++v) {
+            uint32_t ph[4], pl[4], mh[4], ml[4];
+            // A operand [s][t] from [t][s] rows: 16 rows from 16 v, columns from 16 w
+            const uint32_t at = sw_off(kSub * v + ((lane >> 4) << 3) + (lane & 7), 2 * w + ((lane >> 3) & 1));
+            ldsm4t(ph, sp + at);
+            ldsm4t(pl, sp + kTileBytes + at);
+            ldsm4t(mh, sm + at);
+            ldsm4t(ml, sm + kTileBytes + at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t qb[4], kb[4];
+                ldsm4t(qb, step(addr_bt(sq, kSub * v, 0, lane), i));
+                ldsm4t(kb, step(addr_bt(sk, kSub * v, 0, lane), i));
+#pragma unroll
+                for (int u = 0; u < 2; ++u) mma(dk[2 * i + u], pl, qb[2 * u], qb[2 * u + 1]);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) mma(dk[2 * i + u], ml, kb[2 * u], kb[2 * u + 1]);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) mma(dk[2 * i + u], ph, qb[2 * u], qb[2 * u + 1]);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) mma(dk[2 * i + u], mh, kb[2 * u], kb[2 * u + 1]);
+            }
+        }
+        // ---- dbeta and domega of the warp's 16 tokens, a lane a token (lanes 16-31 repeat them)
+        {
+            const int l = lane & 15, t = row + l;
+            // inside the diagonal tile: sums over t' >= t, s < t, by column sums from below
+            float dg = 0.f;
+            if (lane < 16)
+                for (int i = kSub - 1; i > l; --i) s.diag[w][i * 17 + l] = dg += s.diag[w][i * 17 + l];
+            __syncwarp();
+            dg = 0.f;
+            for (int i = 0; i < l; ++i) dg += s.diag[w][l * 17 + i];
+            // rows of this tile from t on, columns of the tiles to the left
+            float rs = __shfl_sync(0xffffffffu, rows0, 4 * (l & 7)), rs1 = __shfl_sync(0xffffffffu, rows1, 4 * (l & 7));
+            rs = l < 8 ? rs : rs1;
+            rs += s.reads[t];
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) {   // from the last token back
+                const float x = __shfl_down_sync(0xffffffffu, rs, o, 16);
+                if (l + o < 16) rs += x;
+            }
+            float later = 0.f;                   // reads of the tiles below
+            for (int i = row + kSub; i < C; ++i) later += s.reads[i];
+            // columns before t in the rows of the tiles below, and the sources before t
+            float before = 0.f;
+            for (int i = lane; i < row; i += 32) {
+                const float bi = s.gates.beta[i];
+                float x = s.kte[i];
+                for (int a = w + 1; a < 4; ++a) x += s.cols[a][i];
+                before = fmaf(bi, x, before);
+            }
+            before = warp_sum(before);
+            float own = s.kte[t];
+            for (int a = w + 1; a < 4; ++a) own += s.cols[a][t];
+            own *= s.gates.beta[t];
+            float pre = own;
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) {
+                const float x = __shfl_up_sync(0xffffffffu, pre, o, 16);
+                if (l >= o) pre += x;
+            }
+            pre = __shfl_up_sync(0xffffffffu, pre, 1, 16);
+            if (l == 0) pre = 0.f;
+            const float gsum = (s.gs[0] + s.gs[1]) + (s.gs[2] + s.gs[3]);
+            const float dl = ((dg + rs) + later) + (before + pre) + s.gates.g[C - 1] * gsum;
+            float db = s.kte[t];
+            for (int a = w; a < 4; ++a) db += s.cols[a][t];
+            if (lane < 16 && t0 + t < T) {
+                const size_t o = ((size_t)b * T + t0 + t) * H + h;
+                ((bf16*)p.g.domega)[o] = __float2bfloat16_rn(-s.gates.rate[t] * dl);
+                ((bf16*)p.g.dbeta)[o] = __float2bfloat16_rn(db);
+            }
+        }
+        __syncthreads();
+    }
+    bf16* oq = (bf16*)p.g.dq + ko;
+    bf16* ok = (bf16*)p.g.dk + ko;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int t = t0 + row + r + 8 * x;
+        if (t >= T) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            *reinterpret_cast<uint32_t*>(oq + (size_t)t * HK * C + 8 * i + c) = pack2(dq[i][2 * x], dq[i][2 * x + 1]);
+            *reinterpret_cast<uint32_t*>(ok + (size_t)t * HK * C + 8 * i + c) = pack2(dk[i][2 * x], dk[i][2 * x + 1]);
+        }
+    }
+}
+
+template <typename Kernel>
+cudaError_t run(Kernel kernel, unsigned grid, int threads, size_t smem, const Args& a, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, threads, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t gdr_backward_tc_bytes(int B, int T, int H) {
+    return (size_t)B * H * ((T + C - 1) / C) * kBlockBytes;
+}
+
+cudaError_t launch_gdr_backward_tc(const GdrIn& in, const float* s_in, const GdrGrads& g, void* ws, cudaStream_t st) {
+    const Args a{in, g, s_in, static_cast<uint8_t*>(ws), (in.T + C - 1) / C};
+    cudaError_t e = run(gated_delta_bwd_chains_kernel, 2u * (unsigned)(in.B * in.H), kTcThreads,
+                        sizeof(ChainSmem) + 1024, a, st);
+    if (e != cudaSuccess) return e;
+    return run(gated_delta_bwd_out_tc_kernel, (unsigned)(in.B * in.HK) * (unsigned)a.blocks, 128,
+               sizeof(OutSmem) + 1024, a, st);
+}
+
+}  // namespace goldwkv
