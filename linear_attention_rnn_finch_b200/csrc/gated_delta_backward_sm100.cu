@@ -9,9 +9,8 @@
 //                 G- = g_16 G + (scale g Q)^T dY - (g K)^T dF,
 //             transposed like the forward one; leaves dV, each block's G and dF.
 // The second, parallel over blocks, forms dQ, dK, dbeta and domega from those with the 64-token
-// forms of the formulas (E and dF are the same values however tokens are grouped).  A warp owns
-// 16 tokens: products with S and G contract value columns, which the chains keep on different
-// warps.
+// forms of the formulas (E and dF are the same values however tokens are grouped).  Its warps own
+// tokens: products with S and G contract value columns, which the chains keep on different warps.
 //
 // S, G, E and dF pass between the launches as two bf16 parts (2^-17 of the value, what the
 // products take anyway) in the order of operand fragments: the chain turns them in registers
@@ -224,10 +223,15 @@ gated_delta_bwd_chains_kernel(const __grid_constant__ Args p) {
 }
 
 // ------------------------------------------------------------------ dQ, dK, dbeta, domega
-// A warp owns tokens 16 w .. 16 w + 15 as rows.  Per value head: products over value columns with
-// S and G, then the 64 x 64 lower triangles, whose rows a warp contracts from its registers and
-// whose columns (dP^T Q, dM^T K) it reads back from shared memory, over S and G's place.  Warp w
-// has w + 1 row and 4 - w column tiles: the same work for each.
+// Eight warps: warp (w, half) owns tokens 16 w .. 16 w + 15 as rows and 32 key channels of dQ and
+// dK.  Per value head: products over value columns with S and G; then the ten 16 x 16 tiles of
+// the lower triangles dP and dM, dealt out to the warps and put, as two bf16 parts, over S and
+// G's place; then their products with K and Q, rows and columns, the same work for every warp.
+// 128 registers and 97 KB: two CTAs an SM, of which one loads while the other computes.  (Four
+// warps with whole rows of keys took 255 registers and left the schedulers two warps each: B8
+// T1024 H32 216 us against XXX.)
+constexpr int kOutThreads = 256;
+
 struct OutSmem {
     uint8_t q[kTileBytes], k[kTileBytes], dy[kTileBytes];
     union {
@@ -238,184 +242,178 @@ struct OutSmem {
             uint8_t dp[2][kTileBytes], dm[2][kTileBytes];   // [t][s], hi and lo parts
         };
     };
-    uint8_t e[kMat];
+    uint8_t e[kMat], df[kMat];
     Gates gates;
-    float cols[4][C];     // column sums of P dY E - M dF E over each warp's rows
-    float reads[C], kte[C];
-    float gs[4];
+    float cols[4][C];      // column sums of P dY E - M dF E over each row tile
+    float rows[4][C];      // [s tile][t]: row sums of the same, times b_s, left of the diagonal
+    float reads[2][C], kte[2][C];
+    float gs[8];
     float diag[4][kSub * 17];
 };
 
-__device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ void get(uint32_t (&r)[4], const uint8_t* p) {
-    const uint4 x = lds128(p);
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
     r[0] = x.x;
     r[1] = x.y;
     r[2] = x.z;
     r[3] = x.w;
 }
 
-__global__ void __launch_bounds__(128, 2)
+__global__ void __launch_bounds__(kOutThreads, 2)
 gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
     extern __shared__ __align__(16) uint8_t raw[];
     OutSmem& s = tiles::smem_aligned<OutSmem>(raw);
     const int n = blockIdx.x % p.blocks, bk = blockIdx.x / p.blocks;
     const int H = p.in.H, HK = p.in.HK, T = p.in.T, b = bk / HK, hk = bk - b * HK, per = H / HK;
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, r = lane >> 2, c = 2 * (lane & 3);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, w = warp & 3, half = warp >> 2;
+    const int r = lane >> 2, c = 2 * (lane & 3);
     const int t0 = n * C, row = kSub * w;
     const size_t ko = ((size_t)b * T * HK + hk) * C;
     const uint32_t sq = ptx::smem_addr(s.q), sk = ptx::smem_addr(s.k), sy = ptx::smem_addr(s.dy);
     const uint32_t sp = ptx::smem_addr(s.dp), sm = ptx::smem_addr(s.dm);
-    copy_block<128>(sq, (const bf16*)p.in.q + ko, (size_t)HK * C, t0, T, tid);
-    copy_block<128>(sk, (const bf16*)p.in.k + ko, (size_t)HK * C, t0, T, tid);
-    float dq[8][4], dk[8][4];
+    copy_block<kOutThreads>(sq, (const bf16*)p.in.q + ko, (size_t)HK * C, t0, T, tid);
+    copy_block<kOutThreads>(sk, (const bf16*)p.in.k + ko, (size_t)HK * C, t0, T, tid);
+    float dq[4][4], dk[4][4];   // key tiles 4 half .. 4 half + 3
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
         clear(dq[i]);
         clear(dk[i]);
     }
     for (int h = hk * per; h < (hk + 1) * per; ++h) {
         const size_t bh = (size_t)b * H + h;
-        const uint8_t* wb = p.ws + (bh * p.blocks + n) * kBlockBytes;
-        copy_block<128>(sy, (const bf16*)p.g.dy + ((size_t)b * T * H + h) * C, (size_t)H * C, t0, T, tid);
+        const uint8_t* wb = p.ws + (bh * p.blocks + n) * kBlockBytes;   // S, E, G, dF
+        copy_block<kOutThreads>(sy, (const bf16*)p.g.dy + ((size_t)b * T * H + h) * C, (size_t)H * C, t0, T, tid);
 #pragma unroll
-        for (int i = 0; i < (int)(kMat / 16 / 128); ++i) {
-            const int o = (i * 128 + tid) * 16;
+        for (int i = 0; i < (int)(kMat / 16 / kOutThreads); ++i) {
+            const int o = (i * kOutThreads + tid) * 16;
             cp_async16(ptx::smem_addr(s.s) + o, wb + o, true);
-            cp_async16(ptx::smem_addr(s.g) + o, wb + 2 * kMat + o, true);
             cp_async16(ptx::smem_addr(s.e) + o, wb + kMat + o, true);
+            cp_async16(ptx::smem_addr(s.g) + o, wb + 2 * kMat + o, true);
+            cp_async16(ptx::smem_addr(s.df) + o, wb + 3 * kMat + o, true);
         }
         cp_async_commit();
-        // this warp's rows of dF, in two parts
-        uint32_t fh[4][4], fl[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint8_t* at = wb + 3 * kMat + ((w * 4 + i) * 32 + lane) * 16;
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
-            const uint4 y = __ldg(reinterpret_cast<const uint4*>(at + kPart));
-            fh[i][0] = x.x; fh[i][1] = x.y; fh[i][2] = x.z; fh[i][3] = x.w;
-            fl[i][0] = y.x; fl[i][1] = y.y; fl[i][2] = y.z; fl[i][3] = y.w;
-        }
         load_gates(s.gates, (const bf16*)p.in.omega, (const bf16*)p.in.beta, (size_t)b * T * H + h, H, t0, T);
         cp_async_wait<0>();
         __syncthreads();
 
-        // ---- with the states: dQ += scale g (dY S^T), dK += b to_end (E G^T) - g (dF S^T)
-        const float g0 = s.gates.g[row + r], g1 = s.gates.g[row + r + 8];
-        const float e0 = s.gates.to_end[row + r], e1 = s.gates.to_end[row + r + 8];
-        const float b0 = s.gates.beta[row + r], b1 = s.gates.beta[row + r + 8];
-        float rd0 = 0.f, rd1 = 0.f, ke0 = 0.f, ke1 = 0.f;
-        uint32_t ya[4][4];
+        // ---- with the states: dK += b to_end (E G^T), then dQ += scale g (dY S^T), dK -= g (dF S^T)
+        const float gt[2] = {s.gates.g[row + r], s.gates.g[row + r + 8]};
+        {
+            const float te[2] = {s.gates.to_end[row + r], s.gates.to_end[row + r + 8]};
+            const float bt[2] = {s.gates.beta[row + r], s.gates.beta[row + r + 8]};
+            float x[4][4], ke[2] = {0.f, 0.f}, gs = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ldsm4(ya[i], step(addr_a(sy, row, 0, lane), i));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {   // two key tiles
-            float a[2][4], f[2][4], eg[2][4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                clear(a[u]);
-                clear(f[u]);
-                clear(eg[u]);
-            }
+            for (int i = 0; i < 4; ++i) clear(x[i]);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {   // 16 value columns
-                uint32_t sh[4], sl[4], gh[4], gl[4], eh[4], el[4];
-                const int o = ((m * 4 + i) * 32 + lane) * 16;
-                get(sh, s.s + o);
-                get(sl, s.s + kPart + o);
-                get(gh, s.g + o);
-                get(gl, s.g + kPart + o);
-                get(eh, s.e + ((w * 4 + m) * 32 + lane) * 16);
-                get(el, s.e + kPart + ((w * 4 + m) * 32 + lane) * 16);
+                uint32_t ah[4], al[4];
+                get(ah, s.e + ((w * 4 + m) * 32 + lane) * 16);
+                get(al, s.e + kPart + ((w * 4 + m) * 32 + lane) * 16);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    mma(a[u], ya[m], sl[2 * u], sl[2 * u + 1]);
-                    mma(f[u], fl[m], sh[2 * u], sh[2 * u + 1]);
-                    mma(eg[u], el, gh[2 * u], gh[2 * u + 1]);
-                }
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t gh[4], gl[4];
+                    const int o = ((m * 4 + 2 * half + i) * 32 + lane) * 16;
+                    get(gh, s.g + o);
+                    get(gl, s.g + kPart + o);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    mma(a[u], ya[m], sh[2 * u], sh[2 * u + 1]);
-                    mma(f[u], fh[m], sl[2 * u], sl[2 * u + 1]);
-                    mma(eg[u], eh, gl[2 * u], gl[2 * u + 1]);
-                }
+                    for (int u = 0; u < 2; ++u) mma(x[2 * i + u], al, gh[2 * u], gh[2 * u + 1]);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    mma(f[u], fh[m], sh[2 * u], sh[2 * u + 1]);
-                    mma(eg[u], eh, gh[2 * u], gh[2 * u + 1]);
-                }
-            }
+                    for (int u = 0; u < 2; ++u) mma(x[2 * i + u], ah, gl[2 * u], gl[2 * u + 1]);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int kt = 2 * i + u;
-                const float2 q0 = tiles::unpack2(tiles::lds32(s.q, sw_off(row + r, kt) + 2 * c));
-                const float2 q1 = tiles::unpack2(tiles::lds32(s.q, sw_off(row + r + 8, kt) + 2 * c));
-                const float2 k0 = tiles::unpack2(tiles::lds32(s.k, sw_off(row + r, kt) + 2 * c));
-                const float2 k1 = tiles::unpack2(tiles::lds32(s.k, sw_off(row + r + 8, kt) + 2 * c));
-                const float qv[4] = {q0.x, q0.y, q1.x, q1.y}, kv[4] = {k0.x, k0.y, k1.x, k1.y};
+                    for (int u = 0; u < 2; ++u) mma(x[2 * i + u], ah, gh[2 * u], gh[2 * u + 1]);
+                    if (m == w) {   // <G, S>: 16 value columns of this half of the keys
+                        uint32_t sh[4], sl[4];
+                        get(sh, s.s + o);
+                        get(sl, s.s + kPart + o);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float g = x < 2 ? g0 : g1, te = x < 2 ? e0 : e1, bt = x < 2 ? b0 : b1;
-                    const float av = p.in.scale * g * a[u][x], fv = g * f[u][x], ev = te * eg[u][x];
-                    dq[kt][x] += av;
-                    dk[kt][x] += fmaf(bt, ev, -fv);
-                    const float rd = fmaf(qv[x], av, -kv[x] * fv), ke = kv[x] * ev;
-                    if (x < 2) {
-                        rd0 += rd;
-                        ke0 += ke;
-                    } else {
-                        rd1 += rd;
-                        ke1 += ke;
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 a = tiles::unpack2(sh[e]), d = tiles::unpack2(sl[e]);
+                            const float2 f = tiles::unpack2(gh[e]), g = tiles::unpack2(gl[e]);
+                            gs = fmaf(a.x + d.x, f.x + g.x, gs);
+                            gs = fmaf(a.y + d.y, f.y + g.y, gs);
+                        }
                     }
                 }
             }
-        }
+            gs = warp_sum(gs);
+            if (lane == 0) s.gs[warp] = gs;
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            rd0 += __shfl_xor_sync(0xffffffffu, rd0, o);
-            rd1 += __shfl_xor_sync(0xffffffffu, rd1, o);
-            ke0 += __shfl_xor_sync(0xffffffffu, ke0, o);
-            ke1 += __shfl_xor_sync(0xffffffffu, ke1, o);
-        }
-        if ((lane & 3) == 0) {
-            s.reads[row + r] = rd0;
-            s.reads[row + r + 8] = rd1;
-            s.kte[row + r] = ke0;
-            s.kte[row + r + 8] = ke1;
-        }
-        // <G, S>, 16 value columns a warp
-        float gs = 0.f;
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t sh[4], sl[4], gh[4], gl[4];
-            const int o = ((w * 4 + i) * 32 + lane) * 16;
-            get(sh, s.s + o);
-            get(sl, s.s + kPart + o);
-            get(gh, s.g + o);
-            get(gl, s.g + kPart + o);
+                for (int e = 0; e < 2; ++e) {
+                    const float2 kv = tiles::unpack2(tiles::lds32(s.k, sw_off(row + r + 8 * e, 4 * half + i) + 2 * c));
+                    const float v0 = te[e] * x[i][2 * e], v1 = te[e] * x[i][2 * e + 1];
+                    dk[i][2 * e] = fmaf(bt[e], v0, dk[i][2 * e]);
+                    dk[i][2 * e + 1] = fmaf(bt[e], v1, dk[i][2 * e + 1]);
+                    ke[e] = fmaf(kv.x, v0, fmaf(kv.y, v1, ke[e]));
+                }
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const float2 a = tiles::unpack2(sh[x]), al = tiles::unpack2(sl[x]);
-                const float2 d = tiles::unpack2(gh[x]), dl = tiles::unpack2(gl[x]);
-                gs = fmaf(a.x + al.x, d.x + dl.x, gs);
-                gs = fmaf(a.y + al.y, d.y + dl.y, gs);
+            for (int e = 0; e < 2; ++e) {
+                ke[e] += __shfl_xor_sync(0xffffffffu, ke[e], 1);
+                ke[e] += __shfl_xor_sync(0xffffffffu, ke[e], 2);
+                if ((lane & 3) == 0) s.kte[half][row + r + 8 * e] = ke[e];
             }
         }
-        gs = warp_sum(gs);
-        if (lane == 0) s.gs[w] = gs;
+        {
+            float x[4][4], y[4][4], rd[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                clear(x[i]);
+                clear(y[i]);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                uint32_t fh[4], fl[4], ya[4];
+                ldsm4(ya, step(addr_a(sy, row, 0, lane), m));
+                get(fh, s.df + ((w * 4 + m) * 32 + lane) * 16);
+                get(fl, s.df + kPart + ((w * 4 + m) * 32 + lane) * 16);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t sh[4], sl[4];
+                    const int o = ((m * 4 + 2 * half + i) * 32 + lane) * 16;
+                    get(sh, s.s + o);
+                    get(sl, s.s + kPart + o);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        mma(x[2 * i + u], fl, sh[2 * u], sh[2 * u + 1]);
+                        mma(y[2 * i + u], ya, sl[2 * u], sl[2 * u + 1]);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) mma(x[2 * i + u], fh, sl[2 * u], sl[2 * u + 1]);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        mma(y[2 * i + u], ya, sh[2 * u], sh[2 * u + 1]);
+                        mma(x[2 * i + u], fh, sh[2 * u], sh[2 * u + 1]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t o = sw_off(row + r + 8 * e, 4 * half + i) + 2 * c;
+                    const float2 qv = tiles::unpack2(tiles::lds32(s.q, o)), kv = tiles::unpack2(tiles::lds32(s.k, o));
+                    const float sg = p.in.scale * gt[e];
+                    const float y0 = sg * y[i][2 * e], y1 = sg * y[i][2 * e + 1];
+                    const float x0 = gt[e] * x[i][2 * e], x1 = gt[e] * x[i][2 * e + 1];
+                    dq[i][2 * e] += y0;
+                    dq[i][2 * e + 1] += y1;
+                    dk[i][2 * e] -= x0;
+                    dk[i][2 * e + 1] -= x1;
+                    rd[e] += (qv.x * y0 - kv.x * x0) + (qv.y * y1 - kv.y * x1);
+                }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                rd[e] += __shfl_xor_sync(0xffffffffu, rd[e], 1);
+                rd[e] += __shfl_xor_sync(0xffffffffu, rd[e], 2);
+                if ((lane & 3) == 0) s.reads[half][row + r + 8 * e] = rd[e];
+            }
+        }
         __syncthreads();   // S and G are read: their place takes dP and dM
 
-        // ---- the triangles, a tile of 16 x 16 at a time
-        uint32_t qa[4][4], ka[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            ldsm4(qa[i], step(addr_a(sq, row, 0, lane), i));
-            ldsm4(ka[i], step(addr_a(sk, row, 0, lane), i));
-        }
-        const float h0 = s.gates.hi[row + r], l0 = s.gates.lo[row + r];
-        const float h1 = s.gates.hi[row + r + 8], l1 = s.gates.lo[row + r + 8];
-        float rows0 = 0.f, rows1 = 0.f;   // sums of W over the tiles left of the diagonal
-        for (int v = 0; v <= w; ++v) {
+        // ---- the triangles: tile (a, v), rows 16 a, columns 16 v; tile number a (a + 1) / 2 + v
+        for (int tile = warp; tile < 10; tile += 8) {
+            const int a = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, v = tile - a * (a + 1) / 2;
             float qk[2][4], kk[2][4], ye[2][4], fe[2][4];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -426,75 +424,93 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t kb[4], eh[4], el[4];
+                uint32_t kb[4], eh[4], el[4], qa[4], ka[4], ya[4], fh[4], fl[4];
                 ldsm4(kb, step(addr_b(sk, kSub * v, 0, lane), i));
+                ldsm4(qa, step(addr_a(sq, kSub * a, 0, lane), i));
+                ldsm4(ka, step(addr_a(sk, kSub * a, 0, lane), i));
+                ldsm4(ya, step(addr_a(sy, kSub * a, 0, lane), i));
+                get(fh, s.df + ((a * 4 + i) * 32 + lane) * 16);
+                get(fl, s.df + kPart + ((a * 4 + i) * 32 + lane) * 16);
                 get(eh, s.e + ((v * 4 + i) * 32 + lane) * 16);
                 get(el, s.e + kPart + ((v * 4 + i) * 32 + lane) * 16);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {   // E's rows as B: registers 0, 2 and 1, 3
-                    mma(qk[u], qa[i], kb[2 * u], kb[2 * u + 1]);
-                    mma(kk[u], ka[i], kb[2 * u], kb[2 * u + 1]);
-                    mma(ye[u], ya[i], el[u], el[u + 2]);
-                    mma(fe[u], fl[i], eh[u], eh[u + 2]);
+                    mma(qk[u], qa, kb[2 * u], kb[2 * u + 1]);
+                    mma(kk[u], ka, kb[2 * u], kb[2 * u + 1]);
+                    mma(ye[u], ya, el[u], el[u + 2]);
+                    mma(fe[u], fl, eh[u], eh[u + 2]);
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    mma(ye[u], ya[i], eh[u], eh[u + 2]);
-                    mma(fe[u], fh[i], el[u], el[u + 2]);
+                    mma(ye[u], ya, eh[u], eh[u + 2]);
+                    mma(fe[u], fh, el[u], el[u + 2]);
                 }
 #pragma unroll
-                for (int u = 0; u < 2; ++u) mma(fe[u], fh[i], eh[u], eh[u + 2]);
+                for (int u = 0; u < 2; ++u) mma(fe[u], fh, eh[u], eh[u + 2]);
             }
-            float cs[4] = {0.f, 0.f, 0.f, 0.f};
+            const int ar = kSub * a + r;
+            const float hh[2] = {s.gates.hi[ar], s.gates.hi[ar + 8]}, ll[2] = {s.gates.lo[ar], s.gates.lo[ar + 8]};
+            float cs[4] = {0.f, 0.f, 0.f, 0.f}, rw[2] = {0.f, 0.f};
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const int cl = 8 * u + c + (x & 1), sc = kSub * v + cl, rl = r + 8 * (x >> 1);
-                    const bool on = v < w || rl >= cl, below = v < w || rl > cl;
-                    const float hh = x < 2 ? h0 : h1, ll = x < 2 ? l0 : l1;
-                    const float d = on ? tiles::fast_exp2((hh - s.gates.hi[sc]) + (ll - s.gates.lo[sc])) : 0.f;
+                    const bool on = v < a || rl >= cl, below = v < a || rl > cl;
+                    const float d = on ? tiles::fast_exp2((hh[x >> 1] - s.gates.hi[sc]) + (ll[x >> 1] - s.gates.lo[sc])) : 0.f;
                     const float bs = s.gates.beta[sc], ds = p.in.scale * d;
                     const float y = on ? ye[u][x] : 0.f, f = below ? fe[u][x] : 0.f;
                     const float sum = ds * qk[u][x] * y - d * kk[u][x] * f;
                     cs[2 * u + (x & 1)] += sum;
                     const float wt = below ? bs * sum : 0.f;
-                    if (v < w) {
-                        if (x < 2) rows0 += wt;
-                        else rows1 += wt;
-                    } else {
-                        s.diag[w][rl * 17 + cl] = wt;
-                    }
+                    rw[x >> 1] += wt;
+                    if (v == a) s.diag[a][rl * 17 + cl] = wt;
                     ye[u][x] = ds * bs * y;      // dP
                     fe[u][x] = -d * bs * f;      // dM
                 }
-            // column sums over the warp's 16 rows
+            // column sums over the tile's rows, row sums over its columns
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) cs[x] += __shfl_xor_sync(0xffffffffu, cs[x], o);
             if (lane < 4) {
-                s.cols[w][kSub * v + c] = cs[0];
-                s.cols[w][kSub * v + c + 1] = cs[1];
-                s.cols[w][kSub * v + 8 + c] = cs[2];
-                s.cols[w][kSub * v + 8 + c + 1] = cs[3];
+                float* at = &s.cols[a][kSub * v + c];
+                at[0] = cs[0];
+                at[1] = cs[1];
+                at[8] = cs[2];
+                at[9] = cs[3];
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                rw[e] += __shfl_xor_sync(0xffffffffu, rw[e], 1);
+                rw[e] += __shfl_xor_sync(0xffffffffu, rw[e], 2);
+                if ((lane & 3) == 0) s.rows[v][ar + 8 * e] = rw[e];   // read where v < a
             }
             uint32_t ph[4], pl[4], mh[4], ml[4];
             split_a(ph, pl, ye[0], ye[1]);
             split_a(mh, ml, fe[0], fe[1]);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const uint32_t o = sw_off(row + r + 8 * (x & 1), 2 * v + (x >> 1)) + 2 * c;
+                const uint32_t o = sw_off(ar + 8 * (x & 1), 2 * v + (x >> 1)) + 2 * c;
                 tiles::sts32(s.dp[0], o, ph[x]);
                 tiles::sts32(s.dp[1], o, pl[x]);
                 tiles::sts32(s.dm[0], o, mh[x]);
                 tiles::sts32(s.dm[1], o, ml[x]);
             }
-            // dQ += dP K, dK += dM K
+        }
+        __syncthreads();
+        // ---- rows: dQ += dP K, dK += dM K
+        for (int v = 0; v <= w; ++v) {
+            uint32_t ph[4], pl[4], mh[4], ml[4];
+            const uint32_t at = addr_a(0, row, 2 * v, lane);
+            ldsm4(ph, sp + at);
+            ldsm4(pl, sp + kTileBytes + at);
+            ldsm4(mh, sm + at);
+            ldsm4(ml, sm + kTileBytes + at);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 uint32_t kb[4];
-                ldsm4t(kb, step(addr_bt(sk, kSub * v, 0, lane), i));
+                ldsm4t(kb, step(addr_bt(sk, kSub * v, 0, lane), 2 * half + i));
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     mma(dq[2 * i + u], pl, kb[2 * u], kb[2 * u + 1]);
@@ -507,12 +523,7 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
                 }
             }
         }
-        rows0 += __shfl_xor_sync(0xffffffffu, rows0, 1);
-        rows1 += __shfl_xor_sync(0xffffffffu, rows1, 1);
-        rows0 += __shfl_xor_sync(0xffffffffu, rows0, 2);
-        rows1 += __shfl_xor_sync(0xffffffffu, rows1, 2);
-        __syncthreads();
-        // ---- their columns: dK += dP^T Q + dM^T K
+        // ---- columns: dK += dP^T Q + dM^T K
         for (int v = w; v < 4; ++v) {
             uint32_t ph[4], pl[4], mh[4], ml[4];
             // A operand [s][t] from [t][s] rows: 16 rows from 16 v, columns from 16 w
@@ -522,10 +533,10 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
             ldsm4t(mh, sm + at);
             ldsm4t(ml, sm + kTileBytes + at);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 uint32_t qb[4], kb[4];
-                ldsm4t(qb, step(addr_bt(sq, kSub * v, 0, lane), i));
-                ldsm4t(kb, step(addr_bt(sk, kSub * v, 0, lane), i));
+                ldsm4t(qb, step(addr_bt(sq, kSub * v, 0, lane), 2 * half + i));
+                ldsm4t(kb, step(addr_bt(sk, kSub * v, 0, lane), 2 * half + i));
 #pragma unroll
                 for (int u = 0; u < 2; ++u) mma(dk[2 * i + u], pl, qb[2 * u], qb[2 * u + 1]);
 #pragma unroll
@@ -536,8 +547,8 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
                 for (int u = 0; u < 2; ++u) mma(dk[2 * i + u], mh, kb[2 * u], kb[2 * u + 1]);
             }
         }
-        // ---- dbeta and domega of the warp's 16 tokens, a lane a token (lanes 16-31 repeat them)
-        {
+        // ---- dbeta and domega of the row tile's 16 tokens, a lane a token (lanes 16-31 repeat them)
+        if (half == 0) {
             const int l = lane & 15, t = row + l;
             // inside the diagonal tile: sums over t' >= t, s < t, by column sums from below
             float dg = 0.f;
@@ -547,29 +558,29 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
             dg = 0.f;
             for (int i = 0; i < l; ++i) dg += s.diag[w][l * 17 + i];
             // rows of this tile from t on, columns of the tiles to the left
-            float rs = __shfl_sync(0xffffffffu, rows0, 4 * (l & 7)), rs1 = __shfl_sync(0xffffffffu, rows1, 4 * (l & 7));
-            rs = l < 8 ? rs : rs1;
-            rs += s.reads[t];
+            float rs = s.reads[0][t] + s.reads[1][t];
+            for (int v = 0; v < w; ++v) rs += s.rows[v][t];
 #pragma unroll
             for (int o = 1; o < 16; o <<= 1) {   // from the last token back
                 const float x = __shfl_down_sync(0xffffffffu, rs, o, 16);
                 if (l + o < 16) rs += x;
             }
             float later = 0.f;                   // reads of the tiles below
-            for (int i = row + kSub; i < C; ++i) later += s.reads[i];
+            for (int i = row + kSub + lane; i < C; i += 32) later += s.reads[0][i] + s.reads[1][i];
             // columns before t in the rows of the tiles below, and the sources before t
             float before = 0.f;
             for (int i = lane; i < row; i += 32) {
-                const float bi = s.gates.beta[i];
-                float x = s.kte[i];
+                float x = s.kte[0][i] + s.kte[1][i];
                 for (int a = w + 1; a < 4; ++a) x += s.cols[a][i];
-                before = fmaf(bi, x, before);
+                before = fmaf(s.gates.beta[i], x, before);
             }
+            later = warp_sum(later);
             before = warp_sum(before);
-            float own = s.kte[t];
+            const float kte = s.kte[0][t] + s.kte[1][t];
+            float own = kte;
             for (int a = w + 1; a < 4; ++a) own += s.cols[a][t];
-            own *= s.gates.beta[t];
-            float pre = own;
+            const float db = own + s.cols[w][t];
+            float pre = s.gates.beta[t] * own;
 #pragma unroll
             for (int o = 1; o < 16; o <<= 1) {
                 const float x = __shfl_up_sync(0xffffffffu, pre, o, 16);
@@ -577,10 +588,10 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
             }
             pre = __shfl_up_sync(0xffffffffu, pre, 1, 16);
             if (l == 0) pre = 0.f;
-            const float gsum = (s.gs[0] + s.gs[1]) + (s.gs[2] + s.gs[3]);
+            float gsum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) gsum += s.gs[i];
             const float dl = ((dg + rs) + later) + (before + pre) + s.gates.g[C - 1] * gsum;
-            float db = s.kte[t];
-            for (int a = w; a < 4; ++a) db += s.cols[a][t];
             if (lane < 16 && t0 + t < T) {
                 const size_t o = ((size_t)b * T + t0 + t) * H + h;
                 ((bf16*)p.g.domega)[o] = __float2bfloat16_rn(-s.gates.rate[t] * dl);
@@ -589,14 +600,14 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
         }
         __syncthreads();
     }
-    bf16* oq = (bf16*)p.g.dq + ko;
-    bf16* ok = (bf16*)p.g.dk + ko;
+    bf16* oq = (bf16*)p.g.dq + ko + 32 * half;
+    bf16* ok = (bf16*)p.g.dk + ko + 32 * half;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int t = t0 + row + r + 8 * x;
         if (t >= T) continue;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             *reinterpret_cast<uint32_t*>(oq + (size_t)t * HK * C + 8 * i + c) = pack2(dq[i][2 * x], dq[i][2 * x + 1]);
             *reinterpret_cast<uint32_t*>(ok + (size_t)t * HK * C + 8 * i + c) = pack2(dk[i][2 * x], dk[i][2 * x + 1]);
         }
@@ -622,7 +633,7 @@ cudaError_t launch_gdr_backward_tc(const GdrIn& in, const float* s_in, const Gdr
     cudaError_t e = run(gated_delta_bwd_chains_kernel, 2u * (unsigned)(in.B * in.H), kTcThreads,
                         sizeof(ChainSmem) + 1024, a, st);
     if (e != cudaSuccess) return e;
-    return run(gated_delta_bwd_out_tc_kernel, (unsigned)(in.B * in.HK) * (unsigned)a.blocks, 128,
+    return run(gated_delta_bwd_out_tc_kernel, (unsigned)(in.B * in.HK) * (unsigned)a.blocks, kOutThreads,
                sizeof(OutSmem) + 1024, a, st);
 }
 
