@@ -642,32 +642,66 @@ def wkv6c2_backward(r, k, v, omega, state_in, dy, dstate_out=None, *, want_dstat
 ACTS = {"none": 0, "silu": 1}
 
 
+# The calls below are short next to what a Python call costs, so they look at each tensor once
+# (_is; the messages are _check's), hand addresses over as plain integers, and change the current
+# device only where it is another one.
+
 def _need_cuda(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("inputs must be CUDA tensors (no CPU implementation)")
 
 
+def _is(name, t, device, dtype, shape):
+    """Checks t and returns its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        _check(name, t, device, dtype, shape)
+    return t.data_ptr()
+
+
+def _optional(name, t, device, dtype, shape):
+    return None if t is None else _is(name, t, device, dtype, shape)
+
+
+def _call(what, fn, device, stream, *args):
+    """fn(*args, stream) with `device` current; raises on an error status."""
+    index = device.index
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, raw)
+    if status != WKV_OK:
+        _raise(what, status)
+
+
+def _workspace(workspace, need, device):
+    """(the workspace, its address, its bytes): a new one of `need` bytes where none is given."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _gdr_args(q, k, v, omega, beta, lead):
-    """Checks of q, k [*lead, HK, D], v [*lead, H, D], omega, beta [*lead, H]; (H, HK, D)."""
+    """Checks of q, k [*lead, HK, D], v [*lead, H, D], omega, beta [*lead, H]; (H, HK, D) and the
+    five addresses."""
     _need_cuda(q, "q")
     if q.dim() != lead + 2 or not isinstance(v, torch.Tensor) or v.dim() != lead + 2:
         raise ValueError("q and v must be " + ("[B, T, heads, D]" if lead == 2 else "[B, heads, D]"))
-    front, HK, D, H = tuple(q.shape[:lead]), q.shape[-2], q.shape[-1], v.shape[-2]
+    shape, H = q.shape, v.shape[-2]
+    front, HK, D = shape[:lead], shape[-2], shape[-1]
     if H and (HK == 0 or H % HK):
         raise ValueError(f"the {H} value heads must be a multiple of the {HK} key heads")
     dev, dt = q.device, q.dtype
-    _check("q", q, dev, dt, (*front, HK, D))
-    _check("k", k, dev, dt, (*front, HK, D))
-    _check("v", v, dev, dt, (*front, H, D))
-    _check("omega", omega, dev, dt, (*front, H))
-    _check("beta", beta, dev, dt, (*front, H))
-    return H, HK, D
-
-
-def _ws_bytes(workspace):
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+    gates = (*front, H)
+    return (H, HK, D), (_is("q", q, dev, dt, shape), _is("k", k, dev, dt, shape),
+                        _is("v", v, dev, dt, (*front, H, D)), _is("omega", omega, dev, dt, gates),
+                        _is("beta", beta, dev, dt, gates))
 
 
 def gated_delta_prefill_workspace_bytes(B, T, H, HK, D, io_dtype) -> int:
@@ -688,28 +722,20 @@ def gated_delta_prefill(q, k, v, omega, beta, state_in=None, *, scale=1.0, y=Non
     ``state_out`` tensor was given.  ``state_out`` may be ``state_in`` (in-place update).
     """
     L = load()
-    H, HK, D = _gdr_args(q, k, v, omega, beta, 2)
+    (H, HK, D), at = _gdr_args(q, k, v, omega, beta, 2)
     B, T = q.shape[:2]
-    dev, dt = q.device, q.dtype
-    if state_in is not None:
-        _check("state_in", state_in, dev, torch.float32, (B, H, D, D))
+    dev, io = q.device, _io(q.dtype)
+    shape = (B, H, D, D)
+    s_in = _optional("state_in", state_in, dev, torch.float32, shape)
     if y is None:
-        y = torch.empty((B, T, H, D), dtype=dt, device=dev)
-    else:
-        _check("y", y, dev, dt, (B, T, H, D))
-    if state_out is not None:
-        _check("state_out", state_out, dev, torch.float32, (B, H, D, D))
-    elif want_state:
-        state_out = torch.empty((B, H, D, D), dtype=torch.float32, device=dev)
-    io = _io(dt)
-    need = int(L.gated_delta_prefill_workspace_bytes(B, T, H, HK, D, io))
-    if workspace is None and need > 0:
-        workspace = new_workspace(need, dev)   # zero: status word
-    with torch.cuda.device(dev):
-        st = L.gated_delta_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(omega), _ptr(beta), float(scale),
-                                   _ptr(state_in), _ptr(state_out), _ptr(y), B, T, H, HK, D, io,
-                                   _ptr(workspace), _ws_bytes(workspace), _stream_ptr(dev, stream))
-    _raise("gated_delta_prefill", st)
+        y = torch.empty_like(v)
+    if state_out is None and want_state:
+        state_out = torch.empty(shape, dtype=torch.float32, device=dev)
+    s_out = _optional("state_out", state_out, dev, torch.float32, shape)
+    workspace, ws, ws_bytes = _workspace(
+        workspace, L.gated_delta_prefill_workspace_bytes(B, T, H, HK, D, io), dev)
+    _call("gated_delta_prefill", L.gated_delta_prefill, dev, stream, *at, float(scale), s_in, s_out,
+          _is("y", y, dev, v.dtype, v.shape), B, T, H, HK, D, io, ws, ws_bytes)
     return y, state_out
 
 
@@ -717,19 +743,13 @@ def gated_delta_decode_step(q, k, v, omega, beta, state, *, scale=1.0, y=None, s
     """One token of the gated delta rule: q, k [B, HK, D], v [B, H, D], omega, beta [B, H];
     ``state`` [B, H, D, D] fp32 is updated in place.  Returns y [B, H, D]."""
     L = load()
-    H, HK, D = _gdr_args(q, k, v, omega, beta, 1)
-    B = q.shape[0]
-    dev, dt = q.device, q.dtype
-    _check("state", state, dev, torch.float32, (B, H, D, D))
+    (H, HK, D), at = _gdr_args(q, k, v, omega, beta, 1)
+    B, dev = q.shape[0], q.device
     if y is None:
-        y = torch.empty((B, H, D), dtype=dt, device=dev)
-    else:
-        _check("y", y, dev, dt, (B, H, D))
-    with torch.cuda.device(dev):
-        st = L.gated_delta_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(omega), _ptr(beta),
-                                       float(scale), _ptr(state), _ptr(y), B, H, HK, D, _io(dt),
-                                       _stream_ptr(dev, stream))
-    _raise("gated_delta_decode_step", st)
+        y = torch.empty_like(v)
+    _call("gated_delta_decode_step", L.gated_delta_decode_step, dev, stream, *at, float(scale),
+          _is("state", state, dev, torch.float32, (B, H, D, D)), _is("y", y, dev, v.dtype, v.shape),
+          B, H, HK, D, _io(q.dtype))
     return y
 
 
@@ -739,52 +759,45 @@ def gated_delta_backward(q, k, v, omega, beta, state_in, dy, dstate_out=None, *,
     state's gradient dstate_out [B, H, D, D] fp32 (None: zero).  Returns (dq, dk, dv, domega,
     dbeta, dstate_in [B, H, D, D] fp32 or None)."""
     L = load()
-    H, HK, D = _gdr_args(q, k, v, omega, beta, 2)
+    (H, HK, D), at = _gdr_args(q, k, v, omega, beta, 2)
     B, T = q.shape[:2]
-    dev, dt = q.device, q.dtype
-    _check("dy", dy, dev, dt, (B, T, H, D))
-    for name, t in (("state_in", state_in), ("dstate_out", dstate_out)):
-        if t is not None:
-            _check(name, t, dev, torch.float32, (B, H, D, D))
+    dev, io = q.device, _io(q.dtype)
+    shape = (B, H, D, D)
+    s_in = _optional("state_in", state_in, dev, torch.float32, shape)
+    ds_out = _optional("dstate_out", dstate_out, dev, torch.float32, shape)
+    dy_at = _is("dy", dy, dev, q.dtype, v.shape)
     dq, dk = torch.empty_like(q), torch.empty_like(k)
     dv, domega, dbeta = torch.empty_like(v), torch.empty_like(omega), torch.empty_like(beta)
-    ds_in = torch.empty((B, H, D, D), dtype=torch.float32, device=dev) if want_dstate_in else None
-    io = _io(dt)
-    need = int(L.gated_delta_backward_workspace_bytes(B, T, H, HK, D, io))
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        st = L.gated_delta_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(omega), _ptr(beta), float(scale),
-                                    _ptr(state_in), _ptr(dy), _ptr(dstate_out), _ptr(dq), _ptr(dk),
-                                    _ptr(dv), _ptr(domega), _ptr(dbeta), _ptr(ds_in), B, T, H, HK,
-                                    D, io, _ptr(workspace), _ws_bytes(workspace),
-                                    _stream_ptr(dev, stream))
-    _raise("gated_delta_backward", st)
+    ds_in = torch.empty(shape, dtype=torch.float32, device=dev) if want_dstate_in else None
+    workspace, ws, ws_bytes = _workspace(
+        workspace, L.gated_delta_backward_workspace_bytes(B, T, H, HK, D, io), dev)
+    _call("gated_delta_backward", L.gated_delta_backward, dev, stream, *at, float(scale), s_in, dy_at, ds_out,
+          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), domega.data_ptr(), dbeta.data_ptr(),
+          None if ds_in is None else ds_in.data_ptr(), B, T, H, HK, D, io, ws, ws_bytes)
     return dq, dk, dv, domega, dbeta, ds_in
 
 
 # ------------------------------------------------------------------ group norm with an activation
 
-def _gn_sizes(x, gamma, beta, groups, act, gate):
-    """Checks of x [N, ..., C] and its parameters; (N, L, C)."""
+def _gn_args(x, gamma, beta, groups, act, gate):
+    """Checks of x [N, ..., C] and its parameters; (N, L, C), the activation's code and the
+    addresses of x, gamma, beta, gate."""
     _need_cuda(x, "x")
-    if x.dim() < 2:
+    shape = x.shape
+    if len(shape) < 2:
         raise ValueError("x must be [N, ..., C]")
-    N, C = x.shape[0], x.shape[-1]
+    N, C, L = shape[0], shape[-1], 1
     if C == 0 or groups <= 0 or C % groups:
         raise ValueError(f"the {C} channels must be a positive multiple of groups ({groups})")
-    if act not in ACTS:
+    code = ACTS.get(act)
+    if code is None:
         raise ValueError(f"unknown activation {act!r}; expected one of {sorted(ACTS)}")
-    L = 1
-    for n in x.shape[1:-1]:
+    for n in shape[1:-1]:
         L *= n
     dev, dt = x.device, x.dtype
-    _check("x", x, dev, dt)
-    _check("gamma", gamma, dev, torch.float32, (C,))
-    _check("beta", beta, dev, torch.float32, (C,))
-    if gate is not None:
-        _check("gate", gate, dev, dt, tuple(x.shape))
-    return N, L, C
+    return (N, L, C), code, (_is("x", x, dev, dt, shape), _is("gamma", gamma, dev, torch.float32, (C,)),
+                             _is("beta", beta, dev, torch.float32, (C,)),
+                             _optional("gate", gate, dev, dt, shape))
 
 
 def group_norm_act(x, gamma, beta, eps=1e-5, *, groups, act="silu", gate=None, y=None,
@@ -794,22 +807,15 @@ def group_norm_act(x, gamma, beta, eps=1e-5, *, groups, act="silu", gate=None, y
     adjacent channels over all positions between, gamma and beta [C] fp32, then ``act`` ("silu"
     or "none") of the result, or with ``gate`` (like x) the result times act(gate).  Every
     token's heads on their own: x [tokens, C], groups = heads.  Returns y."""
-    L_ = load()
-    N, L, C = _gn_sizes(x, gamma, beta, groups, act, gate)
-    dev, dt = x.device, x.dtype
+    lib = load()
+    (N, L, C), code, (x_at, g_at, b_at, gate_at) = _gn_args(x, gamma, beta, groups, act, gate)
+    dev, io = x.device, _io(x.dtype)
     if y is None:
         y = torch.empty_like(x)
-    else:
-        _check("y", y, dev, dt, tuple(x.shape))
-    io = _io(dt)
-    need = int(L_.group_norm_act_workspace_bytes(N, L, C, groups, io)) if L != 1 else 0
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        st = L_.group_norm_act(_ptr(x), _ptr(gamma), _ptr(beta), float(eps), ACTS[act], _ptr(gate),
-                               _ptr(y), N, L, C, groups, io, _ptr(workspace), _ws_bytes(workspace),
-                               _stream_ptr(dev, stream))
-    _raise("group_norm_act", st)
+    need = lib.group_norm_act_workspace_bytes(N, L, C, groups, io) if L != 1 else 0
+    workspace, ws, ws_bytes = _workspace(workspace, need, dev)
+    _call("group_norm_act", lib.group_norm_act, dev, stream, x_at, g_at, b_at, float(eps), code, gate_at,
+          _is("y", y, dev, x.dtype, x.shape), N, L, C, groups, io, ws, ws_bytes)
     return y
 
 
@@ -817,28 +823,22 @@ def group_norm_act_backward(x, gamma, beta, eps, dy, *, groups, act="silu", gate
                             workspace=None, stream=None):
     """Gradients of group_norm_act for dy (like x): (dx, dgamma [C] fp32, dbeta [C] fp32, dgate
     or None).  The statistics are formed again from x."""
-    L_ = load()
-    N, L, C = _gn_sizes(x, gamma, beta, groups, act, gate)
-    dev, dt = x.device, x.dtype
-    _check("dy", dy, dev, dt, tuple(x.shape))
-    dx = torch.empty_like(x)
-    dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(beta)
+    lib = load()
+    (N, L, C), code, (x_at, g_at, b_at, gate_at) = _gn_args(x, gamma, beta, groups, act, gate)
+    dev, io = x.device, _io(x.dtype)
+    dy_at = _is("dy", dy, dev, x.dtype, x.shape)
+    dx, dgamma, dbeta = torch.empty_like(x), torch.empty_like(gamma), torch.empty_like(beta)
     dgate = None if gate is None else torch.empty_like(x)
-    io = _io(dt)
-    need = int(L_.group_norm_act_backward_workspace_bytes(N, L, C, groups, io))
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        st = L_.group_norm_act_backward(_ptr(x), _ptr(gamma), _ptr(beta), float(eps), ACTS[act],
-                                        _ptr(gate), _ptr(dy), _ptr(dx), _ptr(dgamma), _ptr(dbeta),
-                                        _ptr(dgate), N, L, C, groups, io, _ptr(workspace),
-                                        _ws_bytes(workspace), _stream_ptr(dev, stream))
-    _raise("group_norm_act_backward", st)
+    workspace, ws, ws_bytes = _workspace(
+        workspace, lib.group_norm_act_backward_workspace_bytes(N, L, C, groups, io), dev)
+    _call("group_norm_act_backward", lib.group_norm_act_backward, dev, stream, x_at, g_at, b_at, float(eps),
+          code, gate_at, dy_at, dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(),
+          None if dgate is None else dgate.data_ptr(), N, L, C, groups, io, ws, ws_bytes)
     return dx, dgamma, dbeta, dgate
 
 
 def group_norm_act_workspace_bytes(N, L, C, groups, io_dtype, backward=False) -> int:
     """Bytes of workspace group_norm_act (or its backward) needs for x [N, L positions, C]."""
-    L_ = load()
-    fn = L_.group_norm_act_backward_workspace_bytes if backward else L_.group_norm_act_workspace_bytes
+    lib = load()
+    fn = lib.group_norm_act_backward_workspace_bytes if backward else lib.group_norm_act_workspace_bytes
     return int(fn(N, L, C, groups, _io(io_dtype)))
