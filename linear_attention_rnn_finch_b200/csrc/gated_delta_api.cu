@@ -64,11 +64,11 @@ bool gn_sizes_ok(long N, long L, int C, int groups) {
     if (N < 0 || L < 0 || C <= 0 || groups <= 0 || C % groups != 0) return false;
     return true;
 }
-// Grids are one-dimensional: (n, group) pairs and (n, channel tile, split) triples; the
+// Grids are one-dimensional, over (n, channel tile) pairs: at most C / 128 + groups + 1 tiles.  The
 // largest tensors of a 180 GB device stay far below.
 bool gn_sizes_built(long N, long L, int C, int groups) {
     const double most = 2147483647.0;
-    return (double)N * groups <= most && (double)N * (C / 256 + 1) <= most && C <= (1 << 20) &&
+    return (double)N * groups <= most && (L == 1 || (double)N * (C / 128 + groups + 1) <= most) && C <= (1 << 20) &&
            (double)N * (double)L * C < 9e15 && L <= 2147483647L;
 }
 
@@ -168,7 +168,7 @@ wkv_status gated_delta_backward(const void* q, const void* k, const void* v, con
 size_t group_norm_act_workspace_bytes(long N, long L, int C, int groups, wkv_dtype io) {
     if (N <= 0 || L <= 0 || !gn_sizes_ok(N, L, C, groups) || !gn_sizes_built(N, L, C, groups) || !valid_io(io))
         return 0;
-    return goldwkv::group_norm_bytes(N, L, C, groups, io == WKV_BF16);
+    return goldwkv::group_norm_bytes(N, L, C, groups);
 }
 
 static wkv_status check_gn(long N, long L, int C, int groups, wkv_dtype io, float eps, wkv_act act) {
@@ -200,7 +200,7 @@ wkv_status group_norm_act(const void* x, const float* gamma, const float* beta, 
 size_t group_norm_act_backward_workspace_bytes(long N, long L, int C, int groups, wkv_dtype io) {
     if (N <= 0 || L <= 0 || !gn_sizes_ok(N, L, C, groups) || !gn_sizes_built(N, L, C, groups) || !valid_io(io))
         return 0;
-    return goldwkv::group_norm_backward_bytes(N, L, C, groups, io == WKV_BF16);
+    return goldwkv::group_norm_backward_bytes(N, L, C, groups);
 }
 
 wkv_status group_norm_act_backward(const void* x, const float* gamma, const float* beta, float eps,

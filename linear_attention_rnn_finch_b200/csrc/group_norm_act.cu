@@ -9,12 +9,15 @@
 // that a mean far from zero costs no digits.
 //
 // One position (L = 1, each token's heads): a group is a contiguous run of `per` values held
-// in the registers of a few adjacent lanes, read once and written once in one launch.
+// in the registers of a few adjacent lanes, read once and written once in one launch.  A set of
+// lanes keeps its group and walks rows, the next row's loads issued before the present one is
+// worked on, with gamma and beta in registers.
 //
-// Several positions: a thread owns 8 adjacent channels (one, where C is no multiple of 8) and
-// walks positions, so that accesses are whole rows whatever the group's width; it keeps sums
-// per channel, which a small second launch joins into groups, before a third pass applies
-// them.  The positions of one n are cut into as many splits as fill the device.
+// Several positions: a thread owns 8 adjacent channels (one, where the groups do not allow it)
+// and walks positions, so that accesses are whole rows whatever the group's width.  A CTA takes
+// whole groups (or a part of one wide group) over a split of the positions and leaves one
+// (mean, sum of squares about it) a group; the next launch's CTAs join those of their groups
+// themselves.  Two launches forward, three backward.
 #include "common.cuh"
 #include "group_norm_act.h"
 
@@ -99,173 +102,232 @@ __device__ __forceinline__ float lanes_sum(float x, int lanes) {
     return x;
 }
 
+// What a lane loads, before conversion.
+template <typename IO, int V> struct Raw;
+template <> struct Raw<float, 8> { float4 a, b; };
+template <> struct Raw<__nv_bfloat16, 8> { uint4 a; };
+template <> struct Raw<float, 1> { float a; };
+template <> struct Raw<__nv_bfloat16, 1> { __nv_bfloat16 a; };
+template <typename IO, int V>
+__device__ __forceinline__ Raw<IO, V> load_raw(const IO* p) { return *reinterpret_cast<const Raw<IO, V>*>(p); }
+template <int V>
+__device__ __forceinline__ void convert(const Raw<float, V>& r, float (&v)[V]) {
+    const float* p = reinterpret_cast<const float*>(&r);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = p[i];
+}
+__device__ __forceinline__ void convert(const Raw<__nv_bfloat16, 1>& r, float (&v)[1]) { v[0] = __bfloat162float(r.a); }
+__device__ __forceinline__ void convert(const Raw<__nv_bfloat16, 8>& r, float (&v)[8]) {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
 // ------------------------------------------------------------------ one position
 // A group's `units` (of V values) lie on `lanes` adjacent lanes, U a lane (unit = lane +
 // lanes * i), in registers.  U = 0: more than the registers hold, read again for each pass.
+// Set s of lanes keeps group s % groups and takes rows s / groups, + streams, ...
 struct RowShape {
     long rows;       // N
     int C, groups, per, units, lanes;
+    long streams;
 };
+struct RowSet {
+    bool in;
+    int g, l;
+    long n;          // first row
+};
+__device__ __forceinline__ RowSet row_set(const RowShape& s) {
+    RowSet r;
+    const unsigned set = blockIdx.x * (kThreads / s.lanes) + threadIdx.x / s.lanes;
+    r.l = threadIdx.x & (s.lanes - 1);
+    r.n = set / (unsigned)s.groups;
+    r.g = (int)(set - (unsigned)r.n * s.groups);
+    r.in = r.n < s.streams;
+    if (!r.in) r.n = r.g = 0;
+    return r;
+}
 
-// lanes_sum over everything of group g of row n that this lane holds or reads
-template <typename IO, int V, int U>
+template <typename IO, int V, int U, bool kGate>
 __global__ void __launch_bounds__(kThreads)
 group_norm_rows_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
                        const float* __restrict__ gamma, const float* __restrict__ beta, float eps,
                        bool silu, IO* __restrict__ y, RowShape s) {
-    const int per_cta = kThreads / s.lanes;                 // groups a CTA takes
-    const long item = (long)blockIdx.x * per_cta + threadIdx.x / s.lanes;
-    const int l = threadIdx.x & (s.lanes - 1);
-    const bool in = item < s.rows * s.groups;
-    const long n = in ? item / s.groups : 0;
-    const int g = in ? (int)(item - n * s.groups) : 0;
-    const size_t base = (size_t)n * s.C + (size_t)g * s.per;
+    const RowSet set = row_set(s);
+    const int l = set.l, c0 = set.g * s.per;
     const float inv_n = 1.f / (float)s.per;
+    // every lane of a warp runs the same number of rows: the shuffles need them all
+    const long turns = (s.rows + s.streams - 1) / s.streams;
     if (U > 0) {
         constexpr int K = U > 0 ? U : 1;
-        float v[K][V], gt[K][V];
-        float sum = 0.f;
+        float ga[K][V], be[K][V];
+        Raw<IO, V> rx[K], rg[K];
+        bool has[K];
 #pragma unroll
         for (int i = 0; i < K; ++i) {
             const int u = l + s.lanes * i;
-            if (in && u < s.units) {
-                load<V>(x + base + (size_t)u * V, v[i]);
-                if (gate) load<V>(gate + base + (size_t)u * V, gt[i]);
-#pragma unroll
-                for (int e = 0; e < V; ++e) sum += v[i][e];
-            }
-        }
-        const float mean = lanes_sum(sum, s.lanes) * inv_n;
-        float sq = 0.f;
-#pragma unroll
-        for (int i = 0; i < K; ++i)
-            if (in && l + s.lanes * i < s.units) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    v[i][e] -= mean;
-                    sq = fmaf(v[i][e], v[i][e], sq);
-                }
-            }
-        const float r = rsqrtf(lanes_sum(sq, s.lanes) * inv_n + eps);
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-            const int u = l + s.lanes * i;
-            if (in && u < s.units) {
-                float ga[V], be[V];
-                load<V>(gamma + g * s.per + u * V, ga);
-                load<V>(beta + g * s.per + u * V, be);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float z = fmaf(v[i][e] * r, ga[e], be[e]);
-                    v[i][e] = gate ? z * act<IO>(gt[i][e], silu) : act<IO>(z, silu);
-                }
-                store<V>(y + base + (size_t)u * V, v[i]);
-            }
-        }
-    } else {
-        float v[V], gt[V], sum = 0.f, sq = 0.f;
-        if (in)
-            for (int u = l; u < s.units; u += s.lanes) {
-                load<V>(x + base + (size_t)u * V, v);
-#pragma unroll
-                for (int e = 0; e < V; ++e) sum += v[e];
-            }
-        const float mean = lanes_sum(sum, s.lanes) * inv_n;
-        if (in)
-            for (int u = l; u < s.units; u += s.lanes) {
-                load<V>(x + base + (size_t)u * V, v);
-#pragma unroll
-                for (int e = 0; e < V; ++e) sq = fmaf(v[e] - mean, v[e] - mean, sq);
-            }
-        const float r = rsqrtf(lanes_sum(sq, s.lanes) * inv_n + eps);
-        if (in)
-            for (int u = l; u < s.units; u += s.lanes) {
-                float ga[V], be[V];
-                load<V>(x + base + (size_t)u * V, v);
-                if (gate) load<V>(gate + base + (size_t)u * V, gt);
-                load<V>(gamma + g * s.per + u * V, ga);
-                load<V>(beta + g * s.per + u * V, be);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float z = fmaf((v[e] - mean) * r, ga[e], be[e]);
-                    v[e] = gate ? z * act<IO>(gt[e], silu) : act<IO>(z, silu);
-                }
-                store<V>(y + base + (size_t)u * V, v);
-            }
-    }
-}
-
-// Backward over rows: a set of `lanes` lanes keeps one group g and walks rows n = stream,
-// stream + streams, ..., so that its channels' dgamma and dbeta sums stay in registers
-// (U > 0); they leave as one row of partial sums a stream.  U = 0 (wide groups): the sums are
-// kept in the partial row itself, which no one else touches.
-template <typename IO, int V, int U>
-__global__ void __launch_bounds__(kThreads)
-group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
-                           const float* __restrict__ gamma, const float* __restrict__ beta,
-                           float eps, bool silu, const IO* __restrict__ dy, IO* __restrict__ dx,
-                           IO* __restrict__ dgate, float* __restrict__ part, long streams,
-                           RowShape s) {
-    const int per_cta = kThreads / s.lanes;
-    const long set = (long)blockIdx.x * per_cta + threadIdx.x / s.lanes;
-    const int l = threadIdx.x & (s.lanes - 1);
-    const bool in = set < streams * s.groups;
-    const long stream = in ? set / s.groups : 0;
-    const int g = in ? (int)(set - stream * s.groups) : 0;
-    const int c0 = g * s.per;
-    const float inv_n = 1.f / (float)s.per;
-    // partial rows: dgamma then dbeta, [streams][2][C]
-    float* pg = part + (size_t)stream * 2 * s.C + c0;
-    float* pb = pg + s.C;
-    constexpr int K = U > 0 ? U : 1;
-    float dga[K][V], dbe[K][V], ga[K][V], be[K][V];
-#pragma unroll
-    for (int i = 0; i < K; ++i)
-#pragma unroll
-        for (int e = 0; e < V; ++e) dga[i][e] = dbe[i][e] = ga[i][e] = be[i][e] = 0.f;
-    if (U > 0) {
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-            const int u = l + s.lanes * i;
-            if (in && u < s.units) {
+            has[i] = set.in && u < s.units;
+            if (has[i]) {
                 load<V>(gamma + c0 + u * V, ga[i]);
                 load<V>(beta + c0 + u * V, be[i]);
             }
         }
-    } else if (in) {
-        for (int u = l; u < s.units; u += s.lanes) {
-            store<V>(pg + u * V, dga[0]);
-            store<V>(pb + u * V, dga[0]);
-        }
-    }
-    // every lane of a warp runs the same number of rows: the shuffles need them all
-    const long turns = (s.rows + streams - 1) / streams;
-    for (long it = 0; it < turns; ++it) {
-        const long n = stream + it * streams;
-        const bool row = in && n < s.rows;
-        const size_t base = (size_t)(row ? n : 0) * s.C + c0;
-        if (U > 0) {
-            float v[K][V], d[K][V], gt[K][V];
-            float sum = 0.f;
+        auto fetch = [&](long n) {
 #pragma unroll
-            for (int i = 0; i < K; ++i) {
-                const int u = l + s.lanes * i;
-                if (row && u < s.units) {
-                    load<V>(x + base + (size_t)u * V, v[i]);
-                    load<V>(dy + base + (size_t)u * V, d[i]);
-                    if (gate) load<V>(gate + base + (size_t)u * V, gt[i]);
+            for (int i = 0; i < K; ++i)
+                if (has[i] && n < s.rows) {
+                    const size_t o = (size_t)n * s.C + c0 + (l + s.lanes * i) * V;
+                    rx[i] = load_raw<IO, V>(x + o);
+                    if (kGate) rg[i] = load_raw<IO, V>(gate + o);
+                }
+        };
+        long n = set.n;
+        fetch(n);
+        for (long it = 0; it < turns; ++it, n += s.streams) {
+            const bool row = n < s.rows;
+            float v[K][V], gt[K][V], sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+                if (has[i] && row) {
+                    convert(rx[i], v[i]);
+                    if (kGate) convert(rg[i], gt[i]);
 #pragma unroll
                     for (int e = 0; e < V; ++e) sum += v[i][e];
-                } else {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) v[i][e] = d[i][e] = gt[i][e] = 0.f;
                 }
-            }
+            if (it + 1 < turns) fetch(n + s.streams);
             const float mean = lanes_sum(sum, s.lanes) * inv_n;
             float sq = 0.f;
 #pragma unroll
             for (int i = 0; i < K; ++i)
-                if (row && l + s.lanes * i < s.units) {
+                if (has[i] && row) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        v[i][e] -= mean;
+                        sq = fmaf(v[i][e], v[i][e], sq);
+                    }
+                }
+            const float r = rsqrtf(lanes_sum(sq, s.lanes) * inv_n + eps);
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+                if (has[i] && row) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float z = fmaf(v[i][e] * r, ga[i][e], be[i][e]);
+                        v[i][e] = kGate ? z * act<IO>(gt[i][e], silu) : act<IO>(z, silu);
+                    }
+                    store<V>(y + (size_t)n * s.C + c0 + (l + s.lanes * i) * V, v[i]);
+                }
+        }
+    } else {
+        for (long it = 0; it < turns; ++it) {
+            const long n = set.n + it * s.streams;
+            const int units = set.in && n < s.rows ? s.units : 0;
+            const size_t base = (size_t)n * s.C + c0;
+            float v[V], gt[V], sum = 0.f, sq = 0.f;
+            for (int u = l; u < units; u += s.lanes) {
+                load<V>(x + base + (size_t)u * V, v);
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum += v[e];
+            }
+            const float mean = lanes_sum(sum, s.lanes) * inv_n;
+            for (int u = l; u < units; u += s.lanes) {
+                load<V>(x + base + (size_t)u * V, v);
+#pragma unroll
+                for (int e = 0; e < V; ++e) sq = fmaf(v[e] - mean, v[e] - mean, sq);
+            }
+            const float r = rsqrtf(lanes_sum(sq, s.lanes) * inv_n + eps);
+            for (int u = l; u < units; u += s.lanes) {
+                float ga[V], be[V];
+                load<V>(x + base + (size_t)u * V, v);
+                if (kGate) load<V>(gate + base + (size_t)u * V, gt);
+                load<V>(gamma + c0 + u * V, ga);
+                load<V>(beta + c0 + u * V, be);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float z = fmaf((v[e] - mean) * r, ga[e], be[e]);
+                    v[e] = kGate ? z * act<IO>(gt[e], silu) : act<IO>(z, silu);
+                }
+                store<V>(y + base + (size_t)u * V, v);
+            }
+        }
+    }
+}
+
+// dz and, with a gate, dgate (in gt) of one value: h the normalised value, d the output's gradient.
+template <typename IO, bool kGate>
+__device__ __forceinline__ float value_grad(float h, float ga, float be, float d, float& gt, bool silu) {
+    const float z = fmaf(h, ga, be);
+    if (!kGate) return d * act_grad<IO>(z, silu).y;
+    const float2 a = act_grad<IO>(gt, silu);
+    gt = d * z * a.y;
+    return d * a.x;
+}
+
+// Backward over rows: a set's channels' dgamma and dbeta sums stay in registers (U > 0) and leave
+// as one row of partial sums a stream.  U = 0 (wide groups): the sums are kept in the partial
+// row itself, which no one else touches.
+template <typename IO, int V, int U, bool kGate>
+__global__ void __launch_bounds__(kThreads, U == 1 ? 3 : 1)
+group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
+                           const float* __restrict__ gamma, const float* __restrict__ beta,
+                           float eps, bool silu, const IO* __restrict__ dy, IO* __restrict__ dx,
+                           IO* __restrict__ dgate, float* __restrict__ part, RowShape s) {
+    const RowSet set = row_set(s);
+    const int l = set.l, c0 = set.g * s.per;
+    const float inv_n = 1.f / (float)s.per;
+    // partial rows: dgamma then dbeta, [streams][2][C]
+    float* pg = part + (size_t)set.n * 2 * s.C + c0;
+    float* pb = pg + s.C;
+    const long turns = (s.rows + s.streams - 1) / s.streams;
+    if (U > 0) {
+        constexpr int K = U > 0 ? U : 1;
+        float dga[K][V], dbe[K][V], ga[K][V], be[K][V];
+        Raw<IO, V> rx[K], rd[K], rg[K];
+        bool has[K];
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const int u = l + s.lanes * i;
+            has[i] = set.in && u < s.units;
+#pragma unroll
+            for (int e = 0; e < V; ++e) dga[i][e] = dbe[i][e] = 0.f;
+            if (has[i]) {
+                load<V>(gamma + c0 + u * V, ga[i]);
+                load<V>(beta + c0 + u * V, be[i]);
+            }
+        }
+        auto fetch = [&](long n) {
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+                if (has[i] && n < s.rows) {
+                    const size_t o = (size_t)n * s.C + c0 + (l + s.lanes * i) * V;
+                    rx[i] = load_raw<IO, V>(x + o);
+                    rd[i] = load_raw<IO, V>(dy + o);
+                    if (kGate) rg[i] = load_raw<IO, V>(gate + o);
+                }
+        };
+        long n = set.n;
+        fetch(n);
+        for (long it = 0; it < turns; ++it, n += s.streams) {
+            const bool row = n < s.rows;
+            float v[K][V], d[K][V], gt[K][V], sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+                if (has[i] && row) {
+                    convert(rx[i], v[i]);
+                    convert(rd[i], d[i]);
+                    if (kGate) convert(rg[i], gt[i]);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) sum += v[i][e];
+                }
+            if (it + 1 < turns) fetch(n + s.streams);
+            const float mean = lanes_sum(sum, s.lanes) * inv_n;
+            float sq = 0.f;
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+                if (has[i] && row) {
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
                         v[i][e] -= mean;
@@ -275,21 +337,12 @@ group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
             const float r = rsqrtf(lanes_sum(sq, s.lanes) * inv_n + eps);
             float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-            for (int i = 0; i < K; ++i) {
-                const int u = l + s.lanes * i;
-                const bool has = row && u < s.units;
+            for (int i = 0; i < K; ++i)
+                if (has[i] && row) {
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float h = v[i][e] * r, z = fmaf(h, ga[i][e], be[i][e]);
-                    float dz;
-                    if (gate) {
-                        const float2 a = act_grad<IO>(gt[i][e], silu);
-                        gt[i][e] = d[i][e] * z * a.y;
-                        dz = d[i][e] * a.x;
-                    } else {
-                        dz = d[i][e] * act_grad<IO>(z, silu).y;
-                    }
-                    if (has) {
+                    for (int e = 0; e < V; ++e) {
+                        const float h = v[i][e] * r;
+                        const float dz = value_grad<IO, kGate>(h, ga[i][e], be[i][e], d[i][e], gt[i][e], silu);
                         dga[i][e] = fmaf(dz, h, dga[i][e]);
                         dbe[i][e] += dz;
                         const float dh = dz * ga[i][e];
@@ -298,24 +351,39 @@ group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
                         d[i][e] = dh;
                         v[i][e] = h;
                     }
+                    if (kGate) store<V>(dgate + (size_t)n * s.C + c0 + (l + s.lanes * i) * V, gt[i]);
                 }
-                if (gate && has) store<V>(dgate + base + (size_t)u * V, gt[i]);
-            }
             s1 = lanes_sum(s1, s.lanes) * inv_n;
             s2 = lanes_sum(s2, s.lanes) * inv_n;
 #pragma unroll
-            for (int i = 0; i < K; ++i) {
-                const int u = l + s.lanes * i;
-                if (row && u < s.units) {
+            for (int i = 0; i < K; ++i)
+                if (has[i] && row) {
 #pragma unroll
                     for (int e = 0; e < V; ++e) d[i][e] = r * (d[i][e] - s1 - v[i][e] * s2);
-                    store<V>(dx + base + (size_t)u * V, d[i]);
+                    store<V>(dx + (size_t)n * s.C + c0 + (l + s.lanes * i) * V, d[i]);
                 }
+        }
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (has[i]) {
+                store<V>(pg + (l + s.lanes * i) * V, dga[i]);
+                store<V>(pb + (l + s.lanes * i) * V, dbe[i]);
             }
-        } else {
+    } else {
+        float zero[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) zero[e] = 0.f;
+        if (set.in)
+            for (int u = l; u < s.units; u += s.lanes) {
+                store<V>(pg + u * V, zero);
+                store<V>(pb + u * V, zero);
+            }
+        for (long it = 0; it < turns; ++it) {
+            const long n = set.n + it * s.streams;
+            const int units = set.in && n < s.rows ? s.units : 0;
+            const size_t base = (size_t)n * s.C + c0;
             float v[V], d[V], gt[V], gg[V], bb[V];
             float sum = 0.f, sq = 0.f, s1 = 0.f, s2 = 0.f;
-            const int units = row ? s.units : 0;
             for (int u = l; u < units; u += s.lanes) {
                 load<V>(x + base + (size_t)u * V, v);
 #pragma unroll
@@ -332,21 +400,14 @@ group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
                 for (int u = l; u < units; u += s.lanes) {
                     load<V>(x + base + (size_t)u * V, v);
                     load<V>(dy + base + (size_t)u * V, d);
-                    if (gate) load<V>(gate + base + (size_t)u * V, gt);
+                    if (kGate) load<V>(gate + base + (size_t)u * V, gt);
                     load<V>(gamma + c0 + u * V, gg);
                     load<V>(beta + c0 + u * V, bb);
                     float a1[V], a2[V];
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        const float h = (v[e] - mean) * r, z = fmaf(h, gg[e], bb[e]);
-                        float dz;
-                        if (gate) {
-                            const float2 a = act_grad<IO>(gt[e], silu);
-                            gt[e] = d[e] * z * a.y;
-                            dz = d[e] * a.x;
-                        } else {
-                            dz = d[e] * act_grad<IO>(z, silu).y;
-                        }
+                        const float h = (v[e] - mean) * r;
+                        const float dz = value_grad<IO, kGate>(h, gg[e], bb[e], d[e], gt[e], silu);
                         const float dh = dz * gg[e];
                         a1[e] = dz * h;
                         a2[e] = dz;
@@ -368,7 +429,7 @@ group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
                         }
                         store<V>(pg + u * V, o1);
                         store<V>(pb + u * V, o2);
-                        if (gate) store<V>(dgate + base + (size_t)u * V, gt);
+                        if (kGate) store<V>(dgate + base + (size_t)u * V, gt);
                     } else {
                         store<V>(dx + base + (size_t)u * V, d);
                     }
@@ -380,29 +441,20 @@ group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
             }
         }
     }
-    if (U > 0) {
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-            const int u = l + s.lanes * i;
-            if (in && u < s.units) {
-                store<V>(pg + u * V, dga[i]);
-                store<V>(pb + u * V, dbe[i]);
-            }
-        }
-    }
 }
 
 // dgamma[c], dbeta[c] = the sums of `rows` partial rows ([rows][2][C]), in a fixed order: 32
 // columns a CTA, 8 row lanes each, joined through shared memory.
-__global__ void __launch_bounds__(kThreads)
-group_norm_param_kernel(const float* __restrict__ part, long rows, int C, float* __restrict__ dgamma,
-                        float* __restrict__ dbeta) {
+__device__ __forceinline__ void sum_params(const float* __restrict__ part, long rows, int C, int cta,
+                                           float* __restrict__ dgamma, float* __restrict__ dbeta) {
     __shared__ float red[kThreads / 32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int i = blockIdx.x * 32 + lane;   // column of the 2 C
+    const int i = cta * 32 + lane;   // column of the 2 C
     float acc = 0.f;
-    if (i < 2 * C)
+    if (i < 2 * C) {
+#pragma unroll 8
         for (long r = warp; r < rows; r += kThreads / 32) acc += part[(size_t)r * 2 * C + i];
+    }
     red[warp][lane] = acc;
     __syncthreads();
     if (warp == 0 && i < 2 * C) {
@@ -413,47 +465,101 @@ group_norm_param_kernel(const float* __restrict__ part, long rows, int C, float*
         else dbeta[i - C] = t;
     }
 }
+__global__ void __launch_bounds__(kThreads)
+group_norm_param_kernel(const float* __restrict__ part, long rows, int C, float* __restrict__ dgamma,
+                        float* __restrict__ dbeta) {
+    sum_params(part, rows, C, blockIdx.x, dgamma, dbeta);
+}
 
 // ------------------------------------------------------------------ several positions
-// A CTA covers positions [l0, l1) of one n and a tile of up to kThreads channel vectors;
-// thread = (row lane, vector): row lane i walks positions l0 + i, l0 + i + lanes, ...
+// A CTA covers positions [l0, l1) of one n and a tile of at most kThreads channel vectors: whole
+// groups, or one of the `parts` of a group wider than that.  Thread = (row lane, vector): row
+// lane i walks positions l0 + i, l0 + i + lanes, ...
 struct Tiling {
     long N, L;
     int C, groups, per;
-    int vecs;        // channel vectors of the tile in use (all of them when C fits one)
-    int lanes;       // position lanes of the CTA
-    int ctiles;      // channel tiles
+    int V;           // channels of a vector
+    int width;       // channels of a tile
+    int parts;       // tiles of a group (1: a tile holds width / per whole groups)
+    int tiles;       // channel tiles
+    int vecs, lanes; // vectors of a tile, position lanes
     int splits;      // splits of the positions
     long span;       // positions of a split
 };
 struct Place {
     long n;
-    int split, c0;       // first channel of the thread's vector
-    long l0, l1;         // its positions: l0, l0 + lanes, ... < l1
+    int split, tile;
+    int c_begin, c_end;  // the tile's channels
+    int g_begin, g_count;
+    int c0;              // first channel of the thread's vector
+    long first, count;   // the split's positions
+    long l0, l1;         // the thread's: l0, l0 + lanes, ... < l1
     bool in;
 };
-template <int V>
 __device__ __forceinline__ Place place(const Tiling& t) {
     Place p;
-    long i = blockIdx.x;
-    const int ct = (int)(i % t.ctiles);
-    i /= t.ctiles;
-    p.split = (int)(i % t.splits);
-    p.n = i / t.splits;
-    const int lane = threadIdx.x / t.vecs, vec = ct * t.vecs + (threadIdx.x - lane * t.vecs);
-    p.c0 = vec * V;
-    p.l0 = p.split * t.span + lane;
-    p.l1 = min(t.L, (p.split + 1) * t.span);
-    p.in = lane < t.lanes && p.c0 < t.C;
+    const unsigned i = blockIdx.x, ns = i / (unsigned)t.tiles;
+    p.tile = (int)(i - ns * t.tiles);
+    p.n = ns / (unsigned)t.splits;
+    p.split = (int)(ns - (unsigned)p.n * t.splits);
+    if (t.parts == 1) {
+        p.c_begin = p.tile * t.width;
+        p.c_end = min(t.C, p.c_begin + t.width);
+        p.g_begin = p.c_begin / t.per;
+        p.g_count = (p.c_end - p.c_begin) / t.per;
+    } else {
+        p.g_begin = p.tile / t.parts;
+        p.g_count = 1;
+        p.c_begin = p.g_begin * t.per + (p.tile - p.g_begin * t.parts) * t.width;
+        p.c_end = min((p.g_begin + 1) * t.per, p.c_begin + t.width);
+    }
+    const int lane = threadIdx.x / t.vecs;
+    p.c0 = p.c_begin + (threadIdx.x - lane * t.vecs) * t.V;
+    p.first = p.split * t.span;
+    p.count = min(t.L, p.first + t.span) - p.first;
+    p.l0 = p.first + lane;
+    p.l1 = p.first + p.count;
+    p.in = lane < t.lanes && p.c0 < p.c_end;
     return p;
 }
+// Partial sums of group g of n: [n][group][split][part].
+__device__ __forceinline__ size_t partial(const Tiling& t, long n, int g) {
+    return ((size_t)n * t.groups + g) * t.splits * t.parts;
+}
+// Values behind partial i of a group.
+__device__ __forceinline__ float partial_count(const Tiling& t, int i) {
+    const int split = i / t.parts, part = i - split * t.parts;
+    const int channels = t.parts == 1 ? t.per : min(t.width, t.per - part * t.width);
+    return (float)(min(t.L, (split + 1) * t.span) - split * t.span) * (float)channels;
+}
 
-// Per channel of a split: mean and the sum of squares about it.  part [N][splits][C] float2.
+// (mean, 1 / sqrt(var + eps)) of the tile's groups into stat[], a warp a group.
+__device__ __forceinline__ void join_stats(const float2* __restrict__ part, float eps, const Tiling& t,
+                                           const Place& p, float2* stat) {
+    const int lane = threadIdx.x & 31, items = t.splits * t.parts;
+    const float inv = 1.f / ((float)t.L * (float)t.per);
+    for (int g = threadIdx.x >> 5; g < p.g_count; g += kThreads / 32) {
+        const float2* pp = part + partial(t, p.n, p.g_begin + g);
+        float s = 0.f, q = 0.f;
+        for (int i = lane; i < items; i += 32) s = fmaf(partial_count(t, i), pp[i].x, s);
+        const float mean = warp_sum(s) * inv;
+        for (int i = lane; i < items; i += 32) {
+            const float2 r = pp[i];
+            const float d = r.x - mean;
+            q += fmaf(partial_count(t, i) * d, d, r.y);
+        }
+        q = warp_sum(q) * inv;
+        if (lane == 0) stat[g] = make_float2(mean, rsqrtf(q + eps));
+    }
+    __syncthreads();
+}
+
+// A group's mean and sum of squares about it over a split.
 template <typename IO, int V>
 __global__ void __launch_bounds__(kThreads)
 group_norm_stats_kernel(const IO* __restrict__ x, float2* __restrict__ part, Tiling t) {
-    __shared__ float2 red[kThreads * V];   // (lane, vector, element): mean, M2
-    const Place p = place<V>(t);
+    __shared__ float2 red[kThreads * V];   // (lane, channel): mean, M2
+    const Place p = place(t);
     const IO* xp = x + ((size_t)p.n * t.L) * t.C + p.c0;
     float k[V], a[V], q[V];
     int cnt = 0;
@@ -482,79 +588,53 @@ group_norm_stats_kernel(const IO* __restrict__ x, float2* __restrict__ part, Til
     }
     __syncthreads();
     // join the position lanes of each channel
-    const long first = (long)p.split * t.span, have = max(0L, min(t.L, first + t.span) - first);
-    const int ct = (int)(blockIdx.x % t.ctiles), width = t.vecs * V;
-    for (int c = threadIdx.x; c < width; c += kThreads) {
-        const int ch = ct * width + c;
-        if (ch >= t.C) continue;
+    const int width = t.vecs * V, channels = p.c_end - p.c_begin;
+    const int have = (int)min(p.count, (long)t.lanes);   // lanes with a position
+    for (int c = threadIdx.x; c < channels; c += kThreads) {
         float mean = 0.f, m2 = 0.f;
-        for (int i = 0; i < t.lanes; ++i) {
-            const long n_i = have > i ? (have - i + t.lanes - 1) / t.lanes : 0;
-            mean += (float)n_i * red[i * width + c].x;
-        }
-        mean /= (float)have;
-        for (int i = 0; i < t.lanes; ++i) {
-            const long n_i = have > i ? (have - i + t.lanes - 1) / t.lanes : 0;
+        for (int i = 0; i < have; ++i)
+            mean += (float)((p.count - i + t.lanes - 1) / t.lanes) * red[i * width + c].x;
+        mean /= (float)p.count;
+        for (int i = 0; i < have; ++i) {
             const float2 r = red[i * width + c];
             const float d = r.x - mean;
-            m2 += r.y + (float)n_i * d * d;
+            m2 += fmaf((float)((p.count - i + t.lanes - 1) / t.lanes) * d, d, r.y);
         }
-        part[((size_t)p.n * t.splits + p.split) * t.C + ch] = make_float2(mean, m2);
+        red[c] = make_float2(mean, m2);   // lane 0's place: no one else's of this channel
     }
-}
-
-__device__ __forceinline__ float cta_sum(float x, float* red) {
-    x = warp_sum(x);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-    __syncthreads();
-    float t = 0.f;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) t += red[w];
-    return t;
-}
-
-// (mean, 1 / sqrt(var + eps)) of each (n, group) from the channels' partial statistics.
-__global__ void __launch_bounds__(128)
-group_norm_join_stats_kernel(const float2* __restrict__ part, float2* __restrict__ stats, float eps,
-                             Tiling t) {
-    __shared__ float red[4];
-    const long n = blockIdx.x / t.groups;
-    const int g = (int)(blockIdx.x - n * t.groups);
-    const float2* pp = part + (size_t)n * t.splits * t.C + (size_t)g * t.per;
-    const long items = (long)t.splits * t.per;
-    float s = 0.f;
-    for (long i = threadIdx.x; i < items; i += blockDim.x) {
-        const int sp = (int)(i / t.per), c = (int)(i - (long)sp * t.per);
-        const float cnt = (float)(min(t.L, (sp + 1) * t.span) - sp * t.span);
-        s = fmaf(cnt, pp[(size_t)sp * t.C + c].x, s);
+    // and the channels of each group, a warp a group
+    const int lane = threadIdx.x & 31, per = channels / p.g_count;
+    for (int g = threadIdx.x >> 5; g < p.g_count; g += kThreads / 32) {
+        float m = 0.f, q2 = 0.f;
+        for (int c = lane; c < per; c += 32) m += red[g * per + c].x;
+        m = warp_sum(m) / (float)per;
+        for (int c = lane; c < per; c += 32) {
+            const float2 r = red[g * per + c];
+            const float d = r.x - m;
+            q2 += fmaf((float)p.count * d, d, r.y);
+        }
+        q2 = warp_sum(q2);
+        if (lane == 0)
+            part[partial(t, p.n, p.g_begin + g) + (size_t)p.split * t.parts + p.tile % t.parts] = make_float2(m, q2);
     }
-    const float inv = 1.f / ((float)t.L * (float)t.per);
-    const float mean = cta_sum(s, red) * inv;
-    float q = 0.f;
-    for (long i = threadIdx.x; i < items; i += blockDim.x) {
-        const int sp = (int)(i / t.per), c = (int)(i - (long)sp * t.per);
-        const float cnt = (float)(min(t.L, (sp + 1) * t.span) - sp * t.span);
-        const float2 r = pp[(size_t)sp * t.C + c];
-        const float d = r.x - mean;
-        q += fmaf(cnt * d, d, r.y);
-    }
-    const float var = cta_sum(q, red) * inv;
-    if (threadIdx.x == 0) stats[blockIdx.x] = make_float2(mean, rsqrtf(var + eps));
 }
 
 template <typename IO, int V>
 __global__ void __launch_bounds__(kThreads)
 group_norm_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
-                        const float* __restrict__ gamma, const float* __restrict__ beta, bool silu,
-                        const float2* __restrict__ stats, IO* __restrict__ y, Tiling t) {
-    const Place p = place<V>(t);
+                        const float* __restrict__ gamma, const float* __restrict__ beta, float eps,
+                        bool silu, const float2* __restrict__ part, IO* __restrict__ y, Tiling t) {
+    __shared__ float2 stat[kThreads * V];
+    const Place p = place(t);
+    join_stats(part, eps, t, p, stat);
     if (!p.in) return;
     float mean[V], r[V], be[V];
     load<V>(gamma + p.c0, r);
     load<V>(beta + p.c0, be);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const float2 st = stats[p.n * t.groups + (p.c0 + e) / t.per];
+        const float2 st = stat[(p.c0 + e) / t.per - p.g_begin];
         mean[e] = st.x;
         r[e] *= st.y;
     }
@@ -574,29 +654,35 @@ group_norm_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
     }
 }
 
-// Per channel of a split: sums of dz h and of dz; dgate.  part [N][splits][2][C].
+// Per channel of a split: sums of dz h and of dz ([n][split][2][C]); from them each group's sums
+// of dh and dh h; dgate.  The statistics are handed on to the next launch.
 template <typename IO, int V>
 __global__ void __launch_bounds__(kThreads)
 group_norm_bwd_sums_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
-                           const float* __restrict__ gamma, const float* __restrict__ beta,
-                           bool silu, const float2* __restrict__ stats, const IO* __restrict__ dy,
-                           IO* __restrict__ dgate, float* __restrict__ part, Tiling t) {
+                           const float* __restrict__ gamma, const float* __restrict__ beta, float eps,
+                           bool silu, const float2* __restrict__ part, const IO* __restrict__ dy,
+                           IO* __restrict__ dgate, float2* __restrict__ stats,
+                           float* __restrict__ rows, float2* __restrict__ sums, Tiling t) {
     __shared__ float2 red[kThreads * V];
-    const Place p = place<V>(t);
-    float sg[V], sb[V];
+    const Place p = place(t);
+    float2* stat = red;
+    join_stats(part, eps, t, p, stat);
+    if (p.split == 0 && p.tile % t.parts == 0)
+        for (int g = threadIdx.x; g < p.g_count; g += kThreads) stats[p.n * t.groups + p.g_begin + g] = stat[g];
+    float mean[V], r[V], ga[V], be[V], sg[V], sb[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) sg[e] = sb[e] = 0.f;
     if (p.in) {
-        float mean[V], r[V], ga[V], be[V];
         load<V>(gamma + p.c0, ga);
         load<V>(beta + p.c0, be);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const float2 st = stats[p.n * t.groups + (p.c0 + e) / t.per];
+            const float2 st = stat[(p.c0 + e) / t.per - p.g_begin];
             mean[e] = st.x;
             r[e] = st.y;
         }
         const size_t base = ((size_t)p.n * t.L) * t.C + p.c0;
+#pragma unroll 2
         for (long l = p.l0; l < p.l1; l += t.lanes) {
             const size_t o = base + (size_t)l * t.C;
             float v[V], d[V], gt[V];
@@ -605,83 +691,94 @@ group_norm_bwd_sums_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
             if (gate) load<V>(gate + o, gt);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float h = (v[e] - mean[e]) * r[e], z = fmaf(h, ga[e], be[e]);
-                float dz;
-                if (gate) {
-                    const float2 a = act_grad<IO>(gt[e], silu);
-                    gt[e] = d[e] * z * a.y;
-                    dz = d[e] * a.x;
-                } else {
-                    dz = d[e] * act_grad<IO>(z, silu).y;
-                }
+                const float h = (v[e] - mean[e]) * r[e];
+                const float dz = gate ? value_grad<IO, true>(h, ga[e], be[e], d[e], gt[e], silu)
+                                      : value_grad<IO, false>(h, ga[e], be[e], d[e], gt[e], silu);
                 sg[e] = fmaf(dz, h, sg[e]);
                 sb[e] += dz;
             }
             if (gate) store<V>(dgate + o, gt);
         }
     }
+    __syncthreads();   // stat is read
 #pragma unroll
     for (int e = 0; e < V; ++e) red[threadIdx.x * V + e] = make_float2(sg[e], sb[e]);
     __syncthreads();
-    const int ct = (int)(blockIdx.x % t.ctiles), width = t.vecs * V;
-    float* row = part + ((size_t)p.n * t.splits + p.split) * 2 * t.C;
-    for (int c = threadIdx.x; c < width; c += kThreads) {
-        const int ch = ct * width + c;
-        if (ch >= t.C) continue;
+    const int width = t.vecs * V, channels = p.c_end - p.c_begin;
+    float* row = rows + ((size_t)p.n * t.splits + p.split) * 2 * t.C + p.c_begin;
+    for (int c = threadIdx.x; c < channels; c += kThreads) {
         float a = 0.f, b = 0.f;
         for (int i = 0; i < t.lanes; ++i) {
             a += red[i * width + c].x;
             b += red[i * width + c].y;
         }
-        row[ch] = a;
-        row[t.C + ch] = b;
+        row[c] = a;
+        row[t.C + c] = b;
+        const float gm = gamma[p.c_begin + c];
+        red[c] = make_float2(gm * b, gm * a);   // dh, dh h
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 31, per = channels / p.g_count;
+    for (int g = threadIdx.x >> 5; g < p.g_count; g += kThreads / 32) {
+        float s1 = 0.f, s2 = 0.f;
+        for (int c = lane; c < per; c += 32) {
+            s1 += red[g * per + c].x;
+            s2 += red[g * per + c].y;
+        }
+        s1 = warp_sum(s1);
+        s2 = warp_sum(s2);
+        if (lane == 0)
+            sums[partial(t, p.n, p.g_begin + g) + (size_t)p.split * t.parts + p.tile % t.parts] = make_float2(s1, s2);
     }
 }
 
-// (mean(dh), mean(dh h)) of each (n, group).
-__global__ void __launch_bounds__(128)
-group_norm_join_sums_kernel(const float* __restrict__ part, const float* __restrict__ gamma,
-                            float2* __restrict__ sums, Tiling t) {
-    __shared__ float red[4];
-    const long n = blockIdx.x / t.groups;
-    const int g = (int)(blockIdx.x - n * t.groups);
-    const float* pp = part + (size_t)n * t.splits * 2 * t.C + (size_t)g * t.per;
-    const long items = (long)t.splits * t.per;
-    float s1 = 0.f, s2 = 0.f;
-    for (long i = threadIdx.x; i < items; i += blockDim.x) {
-        const int sp = (int)(i / t.per), c = (int)(i - (long)sp * t.per);
-        const float ga = gamma[g * t.per + c];
-        s2 = fmaf(ga, pp[(size_t)sp * 2 * t.C + c], s2);
-        s1 = fmaf(ga, pp[(size_t)sp * 2 * t.C + t.C + c], s1);
-    }
-    s1 = cta_sum(s1, red);
-    s2 = cta_sum(s2, red);
-    const float inv = 1.f / ((float)t.L * (float)t.per);
-    if (threadIdx.x == 0) sums[blockIdx.x] = make_float2(s1 * inv, s2 * inv);
-}
-
+// dx; the CTAs behind the tiles' sum up dgamma and dbeta.
 template <typename IO, int V>
 __global__ void __launch_bounds__(kThreads)
 group_norm_bwd_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
                             const float* __restrict__ gamma, const float* __restrict__ beta,
                             bool silu, const float2* __restrict__ stats,
                             const float2* __restrict__ sums, const IO* __restrict__ dy,
-                            IO* __restrict__ dx, Tiling t) {
-    const Place p = place<V>(t);
+                            IO* __restrict__ dx, const float* __restrict__ rows,
+                            float* __restrict__ dgamma, float* __restrict__ dbeta, unsigned ctas,
+                            Tiling t) {
+    __shared__ float2 sum[kThreads * V];
+    if (blockIdx.x >= ctas) {
+        sum_params(rows, t.N * t.splits, t.C, (int)(blockIdx.x - ctas), dgamma, dbeta);
+        return;
+    }
+    const Place p = place(t);
+    {
+        const int lane = threadIdx.x & 31, items = t.splits * t.parts;
+        const float inv = 1.f / ((float)t.L * (float)t.per);
+        for (int g = threadIdx.x >> 5; g < p.g_count; g += kThreads / 32) {
+            const float2* pp = sums + partial(t, p.n, p.g_begin + g);
+            float s1 = 0.f, s2 = 0.f;
+            for (int i = lane; i < items; i += 32) {
+                s1 += pp[i].x;
+                s2 += pp[i].y;
+            }
+            s1 = warp_sum(s1);
+            s2 = warp_sum(s2);
+            if (lane == 0) sum[g] = make_float2(s1 * inv, s2 * inv);
+        }
+        __syncthreads();
+    }
     if (!p.in) return;
     float mean[V], r[V], ga[V], be[V], s1[V], s2[V];
     load<V>(gamma + p.c0, ga);
     load<V>(beta + p.c0, be);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const long i = p.n * t.groups + (p.c0 + e) / t.per;
-        const float2 st = stats[i], su = sums[i];
+        const int g = (p.c0 + e) / t.per;
+        const float2 st = stats[p.n * t.groups + g], su = sum[g - p.g_begin];
         mean[e] = st.x;
         r[e] = st.y;
         s1[e] = su.x;
         s2[e] = su.y;
     }
     const size_t base = ((size_t)p.n * t.L) * t.C + p.c0;
+#pragma unroll 2
     for (long l = p.l0; l < p.l1; l += t.lanes) {
         const size_t o = base + (size_t)l * t.C;
         float v[V], d[V], gt[V];
@@ -703,13 +800,22 @@ group_norm_bwd_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gat
 constexpr int kSms = 148;
 
 // Registers hold up to 4 vectors of 8 a lane (groups of up to 1024 channels; 2 in the backward),
-// or 8 single values (groups of up to 256).
-RowShape row_shape(long N, int C, int groups) {
-    RowShape s{N, C, groups, C / groups, 0, 1};
+// or 8 single values (groups of up to 256).  Sets of lanes for `ctas` CTAs an SM, and no more
+// streams than rows.
+RowShape row_shape(long N, int C, int groups, int ctas) {
+    RowShape s{N, C, groups, C / groups, 0, 1, 1};
     const int V = s.per % 8 == 0 ? 8 : 1;
     s.units = s.per / V;
     while (s.lanes < s.units && s.lanes < 32) s.lanes *= 2;
+    const long sets = (long)kSms * ctas * (kThreads / s.lanes);
+    const long n = (sets + groups - 1) / groups;
+    s.streams = n < 1 ? 1 : n > N ? N : n;
     return s;
+}
+constexpr int kFwdCtas = 8, kBwdCtas = 3;
+unsigned row_ctas(const RowShape& s) {
+    const int per_cta = kThreads / s.lanes;
+    return (unsigned)((s.streams * s.groups + per_cta - 1) / per_cta);
 }
 int row_units(const RowShape& s) {   // the U of the kernels
     const int need = (s.units + s.lanes - 1) / s.lanes;
@@ -719,56 +825,103 @@ int row_units(const RowShape& s) {   // the U of the kernels
     if (need <= 4) return 4;
     return !vec && need <= 8 ? 8 : 0;
 }
-// Row streams of the backward: enough sets of lanes for four CTAs an SM, and no more than rows.
-long row_streams(const RowShape& s) {
-    const long sets = (long)kSms * 4 * (kThreads / s.lanes);
-    const long n = (sets + s.groups - 1) / s.groups;
-    return n < 1 ? 1 : n > s.rows ? s.rows : n;
-}
+
+int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
 Tiling tiling(long N, long L, int C, int groups) {
-    Tiling t{N, L, C, groups, C / groups, 0, 0, 0, 0, 0};
-    const int V = C % 8 == 0 ? 8 : 1, vecs = C / V;
-    t.vecs = vecs < kThreads ? vecs : kThreads;
+    Tiling t{};
+    t.N = N;
+    t.L = L;
+    t.C = C;
+    t.groups = groups;
+    t.per = C / groups;
+    // vectors of 8 where rows keep them aligned and a tile's bounds can be group bounds too
+    const long unit = (long)t.per * 8 / gcd(t.per, 8);
+    t.V = C % 8 == 0 && (unit <= 8 * kThreads || t.per % 8 == 0) ? 8 : 1;
+    const int most = t.V * kThreads, whole = t.V == 8 ? (int)(unit < most ? unit : most) : t.per;
+    if (t.per <= most) {
+        t.parts = 1;
+        t.width = most / whole * whole;
+        if (t.width > C) t.width = C;
+        t.tiles = (C + t.width - 1) / t.width;
+    } else {
+        t.width = most;
+        t.parts = (t.per + most - 1) / most;
+        t.tiles = groups * t.parts;
+    }
+    t.vecs = (t.width + t.V - 1) / t.V;
     t.lanes = kThreads / t.vecs;
-    t.ctiles = (vecs + t.vecs - 1) / t.vecs;
-    // splits: four CTAs an SM, but at least 8 positions a lane
-    const long ctas = N * t.ctiles;
-    long want = (4L * kSms + ctas - 1) / ctas;
-    const long most = (L + 8L * t.lanes - 1) / (8L * t.lanes);
-    if (want > most) want = most;
+    // splits: two CTAs an SM, but at least 4 positions a lane
+    const long ctas = N * t.tiles;
+    long want = (2L * kSms + ctas - 1) / ctas;
+    const long limit = (L + 4L * t.lanes - 1) / (4L * t.lanes);
+    if (want > limit) want = limit;
     if (want < 1) want = 1;
     t.span = (L + want - 1) / want;
     t.splits = (int)((L + t.span - 1) / t.span);
     return t;
 }
-unsigned tile_ctas(const Tiling& t) { return (unsigned)(t.N * t.splits * t.ctiles); }
+unsigned tile_ctas(const Tiling& t) { return (unsigned)(t.N * t.splits * t.tiles); }
 
 size_t r256(size_t x) { return (x + 255) & ~size_t(255); }
+size_t stats_bytes(const Tiling& t) { return r256((size_t)t.N * t.groups * sizeof(float2)); }
+size_t partial_bytes(const Tiling& t) {
+    return r256((size_t)t.N * t.groups * t.splits * t.parts * sizeof(float2));
+}
 
 template <typename IO, int V, int U>
 cudaError_t rows_fwd(const GroupNorm& a, void* y, const RowShape& s, cudaStream_t st) {
-    const int per_cta = kThreads / s.lanes;
-    const long items = s.rows * s.groups;
-    group_norm_rows_kernel<IO, V, U><<<(unsigned)((items + per_cta - 1) / per_cta), kThreads, 0, st>>>(
-        (const IO*)a.x, (const IO*)a.gate, a.gamma, a.beta, a.eps, a.silu, (IO*)y, s);
+    auto run = [&](auto kernel) {
+        kernel<<<row_ctas(s), kThreads, 0, st>>>((const IO*)a.x, (const IO*)a.gate, a.gamma, a.beta, a.eps,
+                                                 a.silu, (IO*)y, s);
+    };
+    if (a.gate) run(group_norm_rows_kernel<IO, V, U, true>);
+    else run(group_norm_rows_kernel<IO, V, U, false>);
     return cudaGetLastError();
 }
 template <typename IO, int V, int U>
 cudaError_t rows_bwd(const GroupNorm& a, const void* dy, void* dx, void* dgate, float* part,
                      const RowShape& s, cudaStream_t st) {
-    const int per_cta = kThreads / s.lanes;
-    const long streams = row_streams(s), sets = streams * s.groups;
-    group_norm_rows_bwd_kernel<IO, V, U><<<(unsigned)((sets + per_cta - 1) / per_cta), kThreads, 0, st>>>(
-        (const IO*)a.x, (const IO*)a.gate, a.gamma, a.beta, a.eps, a.silu, (const IO*)dy, (IO*)dx,
-        (IO*)dgate, part, streams, s);
+    auto run = [&](auto kernel) {
+        kernel<<<row_ctas(s), kThreads, 0, st>>>((const IO*)a.x, (const IO*)a.gate, a.gamma, a.beta, a.eps,
+                                                 a.silu, (const IO*)dy, (IO*)dx, (IO*)dgate, part, s);
+    };
+    if (a.gate) run(group_norm_rows_bwd_kernel<IO, V, U, true>);
+    else run(group_norm_rows_bwd_kernel<IO, V, U, false>);
+    return cudaGetLastError();
+}
+
+template <typename IO, int V>
+cudaError_t positions_fwd(const GroupNorm& a, void* y, void* ws, const Tiling& t, cudaStream_t st) {
+    float2* part = static_cast<float2*>(ws);
+    const IO* x = (const IO*)a.x;
+    group_norm_stats_kernel<IO, V><<<tile_ctas(t), kThreads, 0, st>>>(x, part, t);
+    group_norm_apply_kernel<IO, V><<<tile_ctas(t), kThreads, 0, st>>>(
+        x, (const IO*)a.gate, a.gamma, a.beta, a.eps, a.silu, part, (IO*)y, t);
+    return cudaGetLastError();
+}
+template <typename IO, int V>
+cudaError_t positions_bwd(const GroupNorm& a, const void* dy, void* dx, float* dgamma, float* dbeta,
+                          void* dgate, void* ws, const Tiling& t, cudaStream_t st) {
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    float2* stats = reinterpret_cast<float2*>(w);
+    float2* part = reinterpret_cast<float2*>(w += stats_bytes(t));
+    float2* sums = reinterpret_cast<float2*>(w += partial_bytes(t));
+    float* rows = reinterpret_cast<float*>(w += partial_bytes(t));
+    const IO *x = (const IO*)a.x, *gate = (const IO*)a.gate, *d = (const IO*)dy;
+    const unsigned grid = tile_ctas(t), params = (unsigned)((2 * t.C + 31) / 32);
+    group_norm_stats_kernel<IO, V><<<grid, kThreads, 0, st>>>(x, part, t);
+    group_norm_bwd_sums_kernel<IO, V><<<grid, kThreads, 0, st>>>(
+        x, gate, a.gamma, a.beta, a.eps, a.silu, part, d, (IO*)dgate, stats, rows, sums, t);
+    group_norm_bwd_apply_kernel<IO, V><<<grid + params, kThreads, 0, st>>>(
+        x, gate, a.gamma, a.beta, a.silu, stats, sums, d, (IO*)dx, rows, dgamma, dbeta, grid, t);
     return cudaGetLastError();
 }
 
 template <typename IO>
 cudaError_t forward_io(const GroupNorm& a, void* y, void* ws, cudaStream_t st) {
     if (a.L == 1) {
-        const RowShape s = row_shape(a.N, a.C, a.groups);
+        const RowShape s = row_shape(a.N, a.C, a.groups, kFwdCtas);
         const int u = row_units(s);
         if (s.per % 8 == 0)
             return u == 1 ? rows_fwd<IO, 8, 1>(a, y, s, st) : u == 2 ? rows_fwd<IO, 8, 2>(a, y, s, st)
@@ -778,31 +931,14 @@ cudaError_t forward_io(const GroupNorm& a, void* y, void* ws, cudaStream_t st) {
              : rows_fwd<IO, 1, 0>(a, y, s, st);
     }
     const Tiling t = tiling(a.N, a.L, a.C, a.groups);
-    float2* stats = static_cast<float2*>(ws);
-    float2* part = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + r256((size_t)a.N * a.groups * sizeof(float2)));
-    const IO* x = (const IO*)a.x;
-    if (a.C % 8 == 0) group_norm_stats_kernel<IO, 8><<<tile_ctas(t), kThreads, 0, st>>>(x, part, t);
-    else group_norm_stats_kernel<IO, 1><<<tile_ctas(t), kThreads, 0, st>>>(x, part, t);
-    group_norm_join_stats_kernel<<<(unsigned)(a.N * a.groups), 128, 0, st>>>(part, stats, a.eps, t);
-    if (a.C % 8 == 0)
-        group_norm_apply_kernel<IO, 8><<<tile_ctas(t), kThreads, 0, st>>>(
-            x, (const IO*)a.gate, a.gamma, a.beta, a.silu, stats, (IO*)y, t);
-    else
-        group_norm_apply_kernel<IO, 1><<<tile_ctas(t), kThreads, 0, st>>>(
-            x, (const IO*)a.gate, a.gamma, a.beta, a.silu, stats, (IO*)y, t);
-    return cudaGetLastError();
-}
-
-cudaError_t params(const float* part, long rows, int C, float* dgamma, float* dbeta, cudaStream_t st) {
-    group_norm_param_kernel<<<(unsigned)((2 * C + 31) / 32), kThreads, 0, st>>>(part, rows, C, dgamma, dbeta);
-    return cudaGetLastError();
+    return t.V == 8 ? positions_fwd<IO, 8>(a, y, ws, t, st) : positions_fwd<IO, 1>(a, y, ws, t, st);
 }
 
 template <typename IO>
 cudaError_t backward_io(const GroupNorm& a, const void* dy, void* dx, float* dgamma, float* dbeta,
                         void* dgate, void* ws, cudaStream_t st) {
     if (a.L == 1) {
-        const RowShape s = row_shape(a.N, a.C, a.groups);
+        const RowShape s = row_shape(a.N, a.C, a.groups, kBwdCtas);
         const int u = row_units(s);
         float* part = static_cast<float*>(ws);
         cudaError_t e;
@@ -817,49 +953,25 @@ cudaError_t backward_io(const GroupNorm& a, const void* dy, void* dx, float* dga
               : u == 8 ? rows_bwd<IO, 1, 8>(a, dy, dx, dgate, part, s, st)
                        : rows_bwd<IO, 1, 0>(a, dy, dx, dgate, part, s, st);
         if (e != cudaSuccess) return e;
-        return params(part, row_streams(s), a.C, dgamma, dbeta, st);
+        group_norm_param_kernel<<<(unsigned)((2 * a.C + 31) / 32), kThreads, 0, st>>>(part, s.streams, a.C,
+                                                                                    dgamma, dbeta);
+        return cudaGetLastError();
     }
     const Tiling t = tiling(a.N, a.L, a.C, a.groups);
-    const size_t sbytes = r256((size_t)a.N * a.groups * sizeof(float2));
-    uint8_t* w = static_cast<uint8_t*>(ws);
-    float2* stats = reinterpret_cast<float2*>(w);
-    float2* sums = reinterpret_cast<float2*>(w + sbytes);
-    float* part = reinterpret_cast<float*>(w + 2 * sbytes);   // statistics, then sums
-    const IO *x = (const IO*)a.x, *gate = (const IO*)a.gate, *d = (const IO*)dy;
-    const unsigned grid = tile_ctas(t), gn = (unsigned)(a.N * a.groups);
-    const bool vec = a.C % 8 == 0;
-    if (vec) group_norm_stats_kernel<IO, 8><<<grid, kThreads, 0, st>>>(x, (float2*)part, t);
-    else group_norm_stats_kernel<IO, 1><<<grid, kThreads, 0, st>>>(x, (float2*)part, t);
-    group_norm_join_stats_kernel<<<gn, 128, 0, st>>>((float2*)part, stats, a.eps, t);
-    if (vec)
-        group_norm_bwd_sums_kernel<IO, 8><<<grid, kThreads, 0, st>>>(
-            x, gate, a.gamma, a.beta, a.silu, stats, d, (IO*)dgate, part, t);
-    else
-        group_norm_bwd_sums_kernel<IO, 1><<<grid, kThreads, 0, st>>>(
-            x, gate, a.gamma, a.beta, a.silu, stats, d, (IO*)dgate, part, t);
-    group_norm_join_sums_kernel<<<gn, 128, 0, st>>>(part, a.gamma, sums, t);
-    if (vec)
-        group_norm_bwd_apply_kernel<IO, 8><<<grid, kThreads, 0, st>>>(
-            x, gate, a.gamma, a.beta, a.silu, stats, sums, d, (IO*)dx, t);
-    else
-        group_norm_bwd_apply_kernel<IO, 1><<<grid, kThreads, 0, st>>>(
-            x, gate, a.gamma, a.beta, a.silu, stats, sums, d, (IO*)dx, t);
-    if (cudaError_t e = cudaGetLastError()) return e;
-    return params(part, a.N * t.splits, a.C, dgamma, dbeta, st);
+    return t.V == 8 ? positions_bwd<IO, 8>(a, dy, dx, dgamma, dbeta, dgate, ws, t, st)
+                    : positions_bwd<IO, 1>(a, dy, dx, dgamma, dbeta, dgate, ws, t, st);
 }
 
 }  // namespace
 
-size_t group_norm_bytes(long N, long L, int C, int groups, bool) {
-    if (L == 1) return 0;
-    const Tiling t = tiling(N, L, C, groups);
-    return r256((size_t)N * groups * sizeof(float2)) + r256((size_t)N * t.splits * C * sizeof(float2));
+size_t group_norm_bytes(long N, long L, int C, int groups) {
+    return L == 1 ? 0 : partial_bytes(tiling(N, L, C, groups));
 }
 
-size_t group_norm_backward_bytes(long N, long L, int C, int groups, bool) {
-    if (L == 1) return r256((size_t)row_streams(row_shape(N, C, groups)) * 2 * C * sizeof(float));
+size_t group_norm_backward_bytes(long N, long L, int C, int groups) {
+    if (L == 1) return r256((size_t)row_shape(N, C, groups, kBwdCtas).streams * 2 * C * sizeof(float));
     const Tiling t = tiling(N, L, C, groups);
-    return 2 * r256((size_t)N * groups * sizeof(float2)) + r256((size_t)N * t.splits * C * sizeof(float2));
+    return stats_bytes(t) + 2 * partial_bytes(t) + r256((size_t)N * t.splits * 2 * C * sizeof(float));
 }
 
 cudaError_t launch_group_norm(const GroupNorm& a, void* y, void* ws, bool bf16, cudaStream_t st) {

@@ -18,10 +18,10 @@ struct GroupNorm {
     int C, groups;
 };
 
-size_t group_norm_bytes(long N, long L, int C, int groups, bool bf16);
+size_t group_norm_bytes(long N, long L, int C, int groups);
 cudaError_t launch_group_norm(const GroupNorm& a, void* y, void* ws, bool bf16, cudaStream_t st);
 
-size_t group_norm_backward_bytes(long N, long L, int C, int groups, bool bf16);
+size_t group_norm_backward_bytes(long N, long L, int C, int groups);
 cudaError_t launch_group_norm_backward(const GroupNorm& a, const void* dy, void* dx, float* dgamma,
                                        float* dbeta, void* dgate, void* ws, bool bf16,
                                        cudaStream_t st);
