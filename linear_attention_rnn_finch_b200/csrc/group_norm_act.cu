@@ -79,12 +79,16 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[V]) {
     }
 }
 
-// sigmoid: the fast exponential and division where the result is rounded to bf16 (relative
-// error about 2^-21), the accurate ones for fp32.
+// sigmoid: the approximate exponential and reciprocal where the result is rounded to bf16
+// (relative error about 2^-21), the accurate ones for fp32.  The gradient over rows issues 40
+// to 70 instructions a value, which bound it before memory did.
 template <typename IO> __device__ __forceinline__ float sigmoid(float x);
 template <> __device__ __forceinline__ float sigmoid<float>(float x) { return 1.f / (1.f + expf(-x)); }
 template <> __device__ __forceinline__ float sigmoid<__nv_bfloat16>(float x) {
-    return __fdividef(1.f, 1.f + __expf(-x));
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
 }
 template <typename IO>
 __device__ __forceinline__ float act(float x, bool silu) { return silu ? x * sigmoid<IO>(x) : x; }
@@ -151,11 +155,11 @@ __device__ __forceinline__ RowSet row_set(const RowShape& s) {
     return r;
 }
 
-template <typename IO, int V, int U, bool kGate>
+template <typename IO, int V, int U, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 group_norm_rows_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
                        const float* __restrict__ gamma, const float* __restrict__ beta, float eps,
-                       bool silu, IO* __restrict__ y, RowShape s) {
+                       IO* __restrict__ y, RowShape s) {
     const RowSet set = row_set(s);
     const int l = set.l, c0 = set.g * s.per;
     const float inv_n = 1.f / (float)s.per;
@@ -175,19 +179,21 @@ group_norm_rows_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
                 load<V>(beta + c0 + u * V, be[i]);
             }
         }
-        auto fetch = [&](long n) {
+        const int apart = s.lanes * V;
+        const size_t stride = (size_t)s.streams * s.C;
+        auto fetch = [&](size_t o) {
 #pragma unroll
             for (int i = 0; i < K; ++i)
-                if (has[i] && n < s.rows) {
-                    const size_t o = (size_t)n * s.C + c0 + (l + s.lanes * i) * V;
-                    rx[i] = load_raw<IO, V>(x + o);
-                    if (kGate) rg[i] = load_raw<IO, V>(gate + o);
+                if (has[i]) {
+                    rx[i] = load_raw<IO, V>(x + o + i * apart);
+                    if (kGate) rg[i] = load_raw<IO, V>(gate + o + i * apart);
                 }
         };
-        long n = set.n;
-        fetch(n);
-        for (long it = 0; it < turns; ++it, n += s.streams) {
-            const bool row = n < s.rows;
+        size_t o = (size_t)set.n * s.C + c0 + l * V;
+        int left = (int)((s.rows - set.n + s.streams - 1) / s.streams);   // rows of this set
+        fetch(o);
+        for (int it = 0; it < turns; ++it, --left, o += stride) {
+            const bool row = left > 0;
             float v[K][V], gt[K][V], sum = 0.f;
 #pragma unroll
             for (int i = 0; i < K; ++i)
@@ -197,7 +203,7 @@ group_norm_rows_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
 #pragma unroll
                     for (int e = 0; e < V; ++e) sum += v[i][e];
                 }
-            if (it + 1 < turns) fetch(n + s.streams);
+            if (left > 1) fetch(o + stride);
             const float mean = lanes_sum(sum, s.lanes) * inv_n;
             float sq = 0.f;
 #pragma unroll
@@ -216,9 +222,9 @@ group_norm_rows_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
                         const float z = fmaf(v[i][e] * r, ga[i][e], be[i][e]);
-                        v[i][e] = kGate ? z * act<IO>(gt[i][e], silu) : act<IO>(z, silu);
+                        v[i][e] = kGate ? z * act<IO>(gt[i][e], kSilu) : act<IO>(z, kSilu);
                     }
-                    store<V>(y + (size_t)n * s.C + c0 + (l + s.lanes * i) * V, v[i]);
+                    store<V>(y + o + i * apart, v[i]);
                 }
         }
     } else {
@@ -248,7 +254,7 @@ group_norm_rows_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float z = fmaf((v[e] - mean) * r, ga[e], be[e]);
-                    v[e] = kGate ? z * act<IO>(gt[e], silu) : act<IO>(z, silu);
+                    v[e] = kGate ? z * act<IO>(gt[e], kSilu) : act<IO>(z, kSilu);
                 }
                 store<V>(y + base + (size_t)u * V, v);
             }
@@ -269,11 +275,11 @@ __device__ __forceinline__ float value_grad(float h, float ga, float be, float d
 // Backward over rows: a set's channels' dgamma and dbeta sums stay in registers (U > 0) and leave
 // as one row of partial sums a stream.  U = 0 (wide groups): the sums are kept in the partial
 // row itself, which no one else touches.
-template <typename IO, int V, int U, bool kGate>
+template <typename IO, int V, int U, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads, U == 1 ? 3 : 1)
 group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
                            const float* __restrict__ gamma, const float* __restrict__ beta,
-                           float eps, bool silu, const IO* __restrict__ dy, IO* __restrict__ dx,
+                           float eps, const IO* __restrict__ dy, IO* __restrict__ dx,
                            IO* __restrict__ dgate, float* __restrict__ part, RowShape s) {
     const RowSet set = row_set(s);
     const int l = set.l, c0 = set.g * s.per;
@@ -298,20 +304,22 @@ group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
                 load<V>(beta + c0 + u * V, be[i]);
             }
         }
-        auto fetch = [&](long n) {
+        const int apart = s.lanes * V;
+        const size_t stride = (size_t)s.streams * s.C;
+        auto fetch = [&](size_t o) {
 #pragma unroll
             for (int i = 0; i < K; ++i)
-                if (has[i] && n < s.rows) {
-                    const size_t o = (size_t)n * s.C + c0 + (l + s.lanes * i) * V;
-                    rx[i] = load_raw<IO, V>(x + o);
-                    rd[i] = load_raw<IO, V>(dy + o);
-                    if (kGate) rg[i] = load_raw<IO, V>(gate + o);
+                if (has[i]) {
+                    rx[i] = load_raw<IO, V>(x + o + i * apart);
+                    rd[i] = load_raw<IO, V>(dy + o + i * apart);
+                    if (kGate) rg[i] = load_raw<IO, V>(gate + o + i * apart);
                 }
         };
-        long n = set.n;
-        fetch(n);
-        for (long it = 0; it < turns; ++it, n += s.streams) {
-            const bool row = n < s.rows;
+        size_t o = (size_t)set.n * s.C + c0 + l * V;
+        int left = (int)((s.rows - set.n + s.streams - 1) / s.streams);   // rows of this set
+        fetch(o);
+        for (int it = 0; it < turns; ++it, --left, o += stride) {
+            const bool row = left > 0;
             float v[K][V], d[K][V], gt[K][V], sum = 0.f;
 #pragma unroll
             for (int i = 0; i < K; ++i)
@@ -322,7 +330,7 @@ group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
 #pragma unroll
                     for (int e = 0; e < V; ++e) sum += v[i][e];
                 }
-            if (it + 1 < turns) fetch(n + s.streams);
+            if (left > 1) fetch(o + stride);
             const float mean = lanes_sum(sum, s.lanes) * inv_n;
             float sq = 0.f;
 #pragma unroll
@@ -342,7 +350,7 @@ group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
                         const float h = v[i][e] * r;
-                        const float dz = value_grad<IO, kGate>(h, ga[i][e], be[i][e], d[i][e], gt[i][e], silu);
+                        const float dz = value_grad<IO, kGate>(h, ga[i][e], be[i][e], d[i][e], gt[i][e], kSilu);
                         dga[i][e] = fmaf(dz, h, dga[i][e]);
                         dbe[i][e] += dz;
                         const float dh = dz * ga[i][e];
@@ -351,7 +359,7 @@ group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
                         d[i][e] = dh;
                         v[i][e] = h;
                     }
-                    if (kGate) store<V>(dgate + (size_t)n * s.C + c0 + (l + s.lanes * i) * V, gt[i]);
+                    if (kGate) store<V>(dgate + o + i * apart, gt[i]);
                 }
             s1 = lanes_sum(s1, s.lanes) * inv_n;
             s2 = lanes_sum(s2, s.lanes) * inv_n;
@@ -360,7 +368,7 @@ group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
                 if (has[i] && row) {
 #pragma unroll
                     for (int e = 0; e < V; ++e) d[i][e] = r * (d[i][e] - s1 - v[i][e] * s2);
-                    store<V>(dx + (size_t)n * s.C + c0 + (l + s.lanes * i) * V, d[i]);
+                    store<V>(dx + o + i * apart, d[i]);
                 }
         }
 #pragma unroll
@@ -407,7 +415,7 @@ group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
                         const float h = (v[e] - mean) * r;
-                        const float dz = value_grad<IO, kGate>(h, gg[e], bb[e], d[e], gt[e], silu);
+                        const float dz = value_grad<IO, kGate>(h, gg[e], bb[e], d[e], gt[e], kSilu);
                         const float dh = dz * gg[e];
                         a1[e] = dz * h;
                         a2[e] = dz;
@@ -444,31 +452,33 @@ group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
 }
 
 // dgamma[c], dbeta[c] = the sums of `rows` partial rows ([rows][2][C]), in a fixed order: 32
-// columns a CTA, 8 row lanes each, joined through shared memory.
+// columns a CTA, kWarps row lanes each, joined through shared memory.
+template <int kWarps>
 __device__ __forceinline__ void sum_params(const float* __restrict__ part, long rows, int C, int cta,
                                            float* __restrict__ dgamma, float* __restrict__ dbeta) {
-    __shared__ float red[kThreads / 32][33];
+    __shared__ float red[kWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i = cta * 32 + lane;   // column of the 2 C
     float acc = 0.f;
     if (i < 2 * C) {
 #pragma unroll 8
-        for (long r = warp; r < rows; r += kThreads / 32) acc += part[(size_t)r * 2 * C + i];
+        for (long r = warp; r < rows; r += kWarps) acc += part[(size_t)r * 2 * C + i];
     }
     red[warp][lane] = acc;
     __syncthreads();
     if (warp == 0 && i < 2 * C) {
         float t = 0.f;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) t += red[w][lane];
+        for (int w = 0; w < kWarps; ++w) t += red[w][lane];
         if (i < C) dgamma[i] = t;
         else dbeta[i - C] = t;
     }
 }
-__global__ void __launch_bounds__(kThreads)
+constexpr int kParamWarps = 32;   // few rows a warp: the loads' latency is all that counts
+__global__ void __launch_bounds__(32 * kParamWarps)
 group_norm_param_kernel(const float* __restrict__ part, long rows, int C, float* __restrict__ dgamma,
                         float* __restrict__ dbeta) {
-    sum_params(part, rows, C, blockIdx.x, dgamma, dbeta);
+    sum_params<kParamWarps>(part, rows, C, blockIdx.x, dgamma, dbeta);
 }
 
 // ------------------------------------------------------------------ several positions
@@ -528,7 +538,7 @@ __device__ __forceinline__ size_t partial(const Tiling& t, long n, int g) {
 }
 // Values behind partial i of a group.
 __device__ __forceinline__ float partial_count(const Tiling& t, int i) {
-    const int split = i / t.parts, part = i - split * t.parts;
+    const int split = t.parts == 1 ? i : i / t.parts, part = i - split * t.parts;
     const int channels = t.parts == 1 ? t.per : min(t.width, t.per - part * t.width);
     return (float)(min(t.L, (split + 1) * t.span) - split * t.span) * (float)channels;
 }
@@ -589,16 +599,16 @@ group_norm_stats_kernel(const IO* __restrict__ x, float2* __restrict__ part, Til
     __syncthreads();
     // join the position lanes of each channel
     const int width = t.vecs * V, channels = p.c_end - p.c_begin;
-    const int have = (int)min(p.count, (long)t.lanes);   // lanes with a position
+    const int count = (int)p.count, each = count / t.lanes, more = count - each * t.lanes;
+    const int have = min(count, t.lanes);   // lanes with a position: each or each + 1 of them
     for (int c = threadIdx.x; c < channels; c += kThreads) {
         float mean = 0.f, m2 = 0.f;
-        for (int i = 0; i < have; ++i)
-            mean += (float)((p.count - i + t.lanes - 1) / t.lanes) * red[i * width + c].x;
-        mean /= (float)p.count;
+        for (int i = 0; i < have; ++i) mean += (float)(each + (i < more)) * red[i * width + c].x;
+        mean /= (float)count;
         for (int i = 0; i < have; ++i) {
             const float2 r = red[i * width + c];
             const float d = r.x - mean;
-            m2 += fmaf((float)((p.count - i + t.lanes - 1) / t.lanes) * d, d, r.y);
+            m2 += fmaf((float)(each + (i < more)) * d, d, r.y);
         }
         red[c] = make_float2(mean, m2);   // lane 0's place: no one else's of this channel
     }
@@ -612,7 +622,7 @@ group_norm_stats_kernel(const IO* __restrict__ x, float2* __restrict__ part, Til
         for (int c = lane; c < per; c += 32) {
             const float2 r = red[g * per + c];
             const float d = r.x - m;
-            q2 += fmaf((float)p.count * d, d, r.y);
+            q2 += fmaf((float)count * d, d, r.y);
         }
         q2 = warp_sum(q2);
         if (lane == 0)
@@ -744,7 +754,7 @@ group_norm_bwd_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gat
                             Tiling t) {
     __shared__ float2 sum[kThreads * V];
     if (blockIdx.x >= ctas) {
-        sum_params(rows, t.N * t.splits, t.C, (int)(blockIdx.x - ctas), dgamma, dbeta);
+        sum_params<kThreads / 32>(rows, t.N * t.splits, t.C, (int)(blockIdx.x - ctas), dgamma, dbeta);
         return;
     }
     const Place p = place(t);
@@ -873,10 +883,10 @@ template <typename IO, int V, int U>
 cudaError_t rows_fwd(const GroupNorm& a, void* y, const RowShape& s, cudaStream_t st) {
     auto run = [&](auto kernel) {
         kernel<<<row_ctas(s), kThreads, 0, st>>>((const IO*)a.x, (const IO*)a.gate, a.gamma, a.beta, a.eps,
-                                                 a.silu, (IO*)y, s);
+                                                 (IO*)y, s);
     };
-    if (a.gate) run(group_norm_rows_kernel<IO, V, U, true>);
-    else run(group_norm_rows_kernel<IO, V, U, false>);
+    if (a.gate) a.silu ? run(group_norm_rows_kernel<IO, V, U, true, true>) : run(group_norm_rows_kernel<IO, V, U, true, false>);
+    else a.silu ? run(group_norm_rows_kernel<IO, V, U, false, true>) : run(group_norm_rows_kernel<IO, V, U, false, false>);
     return cudaGetLastError();
 }
 template <typename IO, int V, int U>
@@ -884,10 +894,10 @@ cudaError_t rows_bwd(const GroupNorm& a, const void* dy, void* dx, void* dgate, 
                      const RowShape& s, cudaStream_t st) {
     auto run = [&](auto kernel) {
         kernel<<<row_ctas(s), kThreads, 0, st>>>((const IO*)a.x, (const IO*)a.gate, a.gamma, a.beta, a.eps,
-                                                 a.silu, (const IO*)dy, (IO*)dx, (IO*)dgate, part, s);
+                                                 (const IO*)dy, (IO*)dx, (IO*)dgate, part, s);
     };
-    if (a.gate) run(group_norm_rows_bwd_kernel<IO, V, U, true>);
-    else run(group_norm_rows_bwd_kernel<IO, V, U, false>);
+    if (a.gate) a.silu ? run(group_norm_rows_bwd_kernel<IO, V, U, true, true>) : run(group_norm_rows_bwd_kernel<IO, V, U, true, false>);
+    else a.silu ? run(group_norm_rows_bwd_kernel<IO, V, U, false, true>) : run(group_norm_rows_bwd_kernel<IO, V, U, false, false>);
     return cudaGetLastError();
 }
 
@@ -953,7 +963,7 @@ cudaError_t backward_io(const GroupNorm& a, const void* dy, void* dx, float* dga
               : u == 8 ? rows_bwd<IO, 1, 8>(a, dy, dx, dgate, part, s, st)
                        : rows_bwd<IO, 1, 0>(a, dy, dx, dgate, part, s, st);
         if (e != cudaSuccess) return e;
-        group_norm_param_kernel<<<(unsigned)((2 * a.C + 31) / 32), kThreads, 0, st>>>(part, s.streams, a.C,
+        group_norm_param_kernel<<<(unsigned)((2 * a.C + 31) / 32), 32 * kParamWarps, 0, st>>>(part, s.streams, a.C,
                                                                                     dgamma, dbeta);
         return cudaGetLastError();
     }
