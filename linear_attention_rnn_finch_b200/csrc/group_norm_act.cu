@@ -18,6 +18,8 @@
 // whole groups (or a part of one wide group) over a split of the positions and leaves one
 // (mean, sum of squares about it) a group; the next launch's CTAs join those of their groups
 // themselves.  Two launches forward, three backward.
+#include <type_traits>
+
 #include "common.cuh"
 #include "group_norm_act.h"
 
@@ -543,23 +545,47 @@ __device__ __forceinline__ float partial_count(const Tiling& t, int i) {
     return (float)(min(t.L, (split + 1) * t.span) - split * t.span) * (float)channels;
 }
 
-// (mean, 1 / sqrt(var + eps)) of the tile's groups into stat[], a warp a group.
+// f(e, group) for the V channels from c0 on.
+template <int V, typename F>
+__device__ __forceinline__ void each_group(const Tiling& t, int c0, F f) {
+    int g = c0 / t.per, left = (g + 1) * t.per - c0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        if (left == 0) {
+            ++g;
+            left = t.per;
+        }
+        --left;
+        f(e, g);
+    }
+}
+// Adjacent lanes that take a group together, so that a tile's groups are joined at once.
+__device__ __forceinline__ int group_lanes(int groups) {
+    int n = 32;
+    while (n > 1 && n * groups > kThreads) n >>= 1;
+    return n;
+}
+// (mean, 1 / sqrt(var + eps)) of the tile's groups into stat[].
 __device__ __forceinline__ void join_stats(const float2* __restrict__ part, float eps, const Tiling& t,
                                            const Place& p, float2* stat) {
-    const int lane = threadIdx.x & 31, items = t.splits * t.parts;
+    const int lanes = group_lanes(p.g_count), lane = threadIdx.x & (lanes - 1), items = t.splits * t.parts;
     const float inv = 1.f / ((float)t.L * (float)t.per);
-    for (int g = threadIdx.x >> 5; g < p.g_count; g += kThreads / 32) {
-        const float2* pp = part + partial(t, p.n, p.g_begin + g);
+    // whole warps run the loop: the shuffles need them
+    for (int g0 = 0; g0 < p.g_count; g0 += kThreads / lanes) {
+        const int g = g0 + threadIdx.x / lanes;
+        const float2* pp = part + partial(t, p.n, p.g_begin + (g < p.g_count ? g : 0));
         float s = 0.f, q = 0.f;
-        for (int i = lane; i < items; i += 32) s = fmaf(partial_count(t, i), pp[i].x, s);
-        const float mean = warp_sum(s) * inv;
-        for (int i = lane; i < items; i += 32) {
+#pragma unroll 4
+        for (int i = lane; i < items; i += lanes) s = fmaf(partial_count(t, i), pp[i].x, s);
+        const float mean = lanes_sum(s, lanes) * inv;
+#pragma unroll 4
+        for (int i = lane; i < items; i += lanes) {
             const float2 r = pp[i];
             const float d = r.x - mean;
             q += fmaf(partial_count(t, i) * d, d, r.y);
         }
-        q = warp_sum(q) * inv;
-        if (lane == 0) stat[g] = make_float2(mean, rsqrtf(q + eps));
+        q = lanes_sum(q, lanes) * inv;
+        if (lane == 0 && g < p.g_count) stat[g] = make_float2(mean, rsqrtf(q + eps));
     }
     __syncthreads();
 }
@@ -577,7 +603,7 @@ group_norm_stats_kernel(const IO* __restrict__ x, float2* __restrict__ part, Til
     for (int e = 0; e < V; ++e) k[e] = a[e] = q[e] = 0.f;
     if (p.in && p.l0 < p.l1) {
         load<V>(xp + (size_t)p.l0 * t.C, k);   // differences from the thread's first values
-#pragma unroll 4
+#pragma unroll 8
         for (long l = p.l0; l < p.l1; l += t.lanes) {
             float v[V];
             load<V>(xp + (size_t)l * t.C, v);
@@ -613,28 +639,29 @@ group_norm_stats_kernel(const IO* __restrict__ x, float2* __restrict__ part, Til
         red[c] = make_float2(mean, m2);   // lane 0's place: no one else's of this channel
     }
     __syncthreads();
-    // and the channels of each group, a warp a group
-    const int lane = threadIdx.x & 31, per = channels / p.g_count;
-    for (int g = threadIdx.x >> 5; g < p.g_count; g += kThreads / 32) {
+    // and the channels of each group
+    const int gl = group_lanes(p.g_count), lane = threadIdx.x & (gl - 1), per = channels / p.g_count;
+    for (int g0 = 0; g0 < p.g_count; g0 += kThreads / gl) {
+        const int g = g0 + threadIdx.x / gl, own = g < p.g_count ? per : 0;
         float m = 0.f, q2 = 0.f;
-        for (int c = lane; c < per; c += 32) m += red[g * per + c].x;
-        m = warp_sum(m) / (float)per;
-        for (int c = lane; c < per; c += 32) {
+        for (int c = lane; c < own; c += gl) m += red[g * per + c].x;
+        m = lanes_sum(m, gl) / (float)per;
+        for (int c = lane; c < own; c += gl) {
             const float2 r = red[g * per + c];
             const float d = r.x - m;
             q2 += fmaf((float)count * d, d, r.y);
         }
-        q2 = warp_sum(q2);
-        if (lane == 0)
+        q2 = lanes_sum(q2, gl);
+        if (lane == 0 && own)
             part[partial(t, p.n, p.g_begin + g) + (size_t)p.split * t.parts + p.tile % t.parts] = make_float2(m, q2);
     }
 }
 
-template <typename IO, int V>
+template <typename IO, int V, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 group_norm_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
                         const float* __restrict__ gamma, const float* __restrict__ beta, float eps,
-                        bool silu, const float2* __restrict__ part, IO* __restrict__ y, Tiling t) {
+                        const float2* __restrict__ part, IO* __restrict__ y, Tiling t) {
     __shared__ float2 stat[kThreads * V];
     const Place p = place(t);
     join_stats(part, eps, t, p, stat);
@@ -642,23 +669,22 @@ group_norm_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
     float mean[V], r[V], be[V];
     load<V>(gamma + p.c0, r);
     load<V>(beta + p.c0, be);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        const float2 st = stat[(p.c0 + e) / t.per - p.g_begin];
+    each_group<V>(t, p.c0, [&](int e, int g) {
+        const float2 st = stat[g - p.g_begin];
         mean[e] = st.x;
         r[e] *= st.y;
-    }
+    });
     const size_t base = ((size_t)p.n * t.L) * t.C + p.c0;
 #pragma unroll 2
     for (long l = p.l0; l < p.l1; l += t.lanes) {
         const size_t o = base + (size_t)l * t.C;
         float v[V], gt[V];
         load<V>(x + o, v);
-        if (gate) load<V>(gate + o, gt);
+        if (kGate) load<V>(gate + o, gt);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const float z = fmaf(v[e] - mean[e], r[e], be[e]);
-            v[e] = gate ? z * act<IO>(gt[e], silu) : act<IO>(z, silu);
+            v[e] = kGate ? z * act<IO>(gt[e], kSilu) : act<IO>(z, kSilu);
         }
         store<V>(y + o, v);
     }
@@ -666,11 +692,11 @@ group_norm_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
 
 // Per channel of a split: sums of dz h and of dz ([n][split][2][C]); from them each group's sums
 // of dh and dh h; dgate.  The statistics are handed on to the next launch.
-template <typename IO, int V>
+template <typename IO, int V, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 group_norm_bwd_sums_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
                            const float* __restrict__ gamma, const float* __restrict__ beta, float eps,
-                           bool silu, const float2* __restrict__ part, const IO* __restrict__ dy,
+                           const float2* __restrict__ part, const IO* __restrict__ dy,
                            IO* __restrict__ dgate, float2* __restrict__ stats,
                            float* __restrict__ rows, float2* __restrict__ sums, Tiling t) {
     __shared__ float2 red[kThreads * V];
@@ -685,12 +711,11 @@ group_norm_bwd_sums_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
     if (p.in) {
         load<V>(gamma + p.c0, ga);
         load<V>(beta + p.c0, be);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float2 st = stat[(p.c0 + e) / t.per - p.g_begin];
+        each_group<V>(t, p.c0, [&](int e, int g) {
+            const float2 st = stat[g - p.g_begin];
             mean[e] = st.x;
             r[e] = st.y;
-        }
+        });
         const size_t base = ((size_t)p.n * t.L) * t.C + p.c0;
 #pragma unroll 2
         for (long l = p.l0; l < p.l1; l += t.lanes) {
@@ -698,16 +723,15 @@ group_norm_bwd_sums_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
             float v[V], d[V], gt[V];
             load<V>(x + o, v);
             load<V>(dy + o, d);
-            if (gate) load<V>(gate + o, gt);
+            if (kGate) load<V>(gate + o, gt);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float h = (v[e] - mean[e]) * r[e];
-                const float dz = gate ? value_grad<IO, true>(h, ga[e], be[e], d[e], gt[e], silu)
-                                      : value_grad<IO, false>(h, ga[e], be[e], d[e], gt[e], silu);
+                const float dz = value_grad<IO, kGate>(h, ga[e], be[e], d[e], gt[e], kSilu);
                 sg[e] = fmaf(dz, h, sg[e]);
                 sb[e] += dz;
             }
-            if (gate) store<V>(dgate + o, gt);
+            if (kGate) store<V>(dgate + o, gt);
         }
     }
     __syncthreads();   // stat is read
@@ -728,26 +752,27 @@ group_norm_bwd_sums_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
         red[c] = make_float2(gm * b, gm * a);   // dh, dh h
     }
     __syncthreads();
-    const int lane = threadIdx.x & 31, per = channels / p.g_count;
-    for (int g = threadIdx.x >> 5; g < p.g_count; g += kThreads / 32) {
+    const int gl = group_lanes(p.g_count), lane = threadIdx.x & (gl - 1), per = channels / p.g_count;
+    for (int g0 = 0; g0 < p.g_count; g0 += kThreads / gl) {
+        const int g = g0 + threadIdx.x / gl, own = g < p.g_count ? per : 0;
         float s1 = 0.f, s2 = 0.f;
-        for (int c = lane; c < per; c += 32) {
+        for (int c = lane; c < own; c += gl) {
             s1 += red[g * per + c].x;
             s2 += red[g * per + c].y;
         }
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
-        if (lane == 0)
+        s1 = lanes_sum(s1, gl);
+        s2 = lanes_sum(s2, gl);
+        if (lane == 0 && own)
             sums[partial(t, p.n, p.g_begin + g) + (size_t)p.split * t.parts + p.tile % t.parts] = make_float2(s1, s2);
     }
 }
 
 // dx; the CTAs behind the tiles' sum up dgamma and dbeta.
-template <typename IO, int V>
+template <typename IO, int V, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 group_norm_bwd_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
                             const float* __restrict__ gamma, const float* __restrict__ beta,
-                            bool silu, const float2* __restrict__ stats,
+                            const float2* __restrict__ stats,
                             const float2* __restrict__ sums, const IO* __restrict__ dy,
                             IO* __restrict__ dx, const float* __restrict__ rows,
                             float* __restrict__ dgamma, float* __restrict__ dbeta, unsigned ctas,
@@ -759,18 +784,20 @@ group_norm_bwd_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gat
     }
     const Place p = place(t);
     {
-        const int lane = threadIdx.x & 31, items = t.splits * t.parts;
+        const int lanes = group_lanes(p.g_count), lane = threadIdx.x & (lanes - 1), items = t.splits * t.parts;
         const float inv = 1.f / ((float)t.L * (float)t.per);
-        for (int g = threadIdx.x >> 5; g < p.g_count; g += kThreads / 32) {
-            const float2* pp = sums + partial(t, p.n, p.g_begin + g);
+        for (int g0 = 0; g0 < p.g_count; g0 += kThreads / lanes) {
+            const int g = g0 + threadIdx.x / lanes;
+            const float2* pp = sums + partial(t, p.n, p.g_begin + (g < p.g_count ? g : 0));
             float s1 = 0.f, s2 = 0.f;
-            for (int i = lane; i < items; i += 32) {
+#pragma unroll 4
+            for (int i = lane; i < items; i += lanes) {
                 s1 += pp[i].x;
                 s2 += pp[i].y;
             }
-            s1 = warp_sum(s1);
-            s2 = warp_sum(s2);
-            if (lane == 0) sum[g] = make_float2(s1 * inv, s2 * inv);
+            s1 = lanes_sum(s1, lanes);
+            s2 = lanes_sum(s2, lanes);
+            if (lane == 0 && g < p.g_count) sum[g] = make_float2(s1 * inv, s2 * inv);
         }
         __syncthreads();
     }
@@ -778,15 +805,13 @@ group_norm_bwd_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gat
     float mean[V], r[V], ga[V], be[V], s1[V], s2[V];
     load<V>(gamma + p.c0, ga);
     load<V>(beta + p.c0, be);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        const int g = (p.c0 + e) / t.per;
+    each_group<V>(t, p.c0, [&](int e, int g) {
         const float2 st = stats[p.n * t.groups + g], su = sum[g - p.g_begin];
         mean[e] = st.x;
         r[e] = st.y;
         s1[e] = su.x;
         s2[e] = su.y;
-    }
+    });
     const size_t base = ((size_t)p.n * t.L) * t.C + p.c0;
 #pragma unroll 2
     for (long l = p.l0; l < p.l1; l += t.lanes) {
@@ -794,12 +819,12 @@ group_norm_bwd_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gat
         float v[V], d[V], gt[V];
         load<V>(x + o, v);
         load<V>(dy + o, d);
-        if (gate) load<V>(gate + o, gt);
+        if (kGate) load<V>(gate + o, gt);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const float h = (v[e] - mean[e]) * r[e];
-            const float dz = d[e] * (gate ? act<IO>(gt[e], silu)
-                                          : act_grad<IO>(fmaf(h, ga[e], be[e]), silu).y);
+            const float dz = d[e] * (kGate ? act<IO>(gt[e], kSilu)
+                                          : act_grad<IO>(fmaf(h, ga[e], be[e]), kSilu).y);
             d[e] = r[e] * (dz * ga[e] - s1[e] - h * s2[e]);
         }
         store<V>(dx + o, d);
@@ -861,7 +886,8 @@ Tiling tiling(long N, long L, int C, int groups) {
     }
     t.vecs = (t.width + t.V - 1) / t.V;
     t.lanes = kThreads / t.vecs;
-    // splits: two CTAs an SM, but at least 4 positions a lane
+    // splits: two CTAs an SM (each pays a few hundred instructions a thread to join its groups:
+    // [8, 4093, 320] 25 us, with three or four 27), but at least 4 positions a lane
     const long ctas = N * t.tiles;
     long want = (2L * kSms + ctas - 1) / ctas;
     const long limit = (L + 4L * t.lanes - 1) / (4L * t.lanes);
@@ -901,16 +927,16 @@ cudaError_t rows_bwd(const GroupNorm& a, const void* dy, void* dx, void* dgate, 
     return cudaGetLastError();
 }
 
-template <typename IO, int V>
+template <typename IO, int V, bool kGate, bool kSilu>
 cudaError_t positions_fwd(const GroupNorm& a, void* y, void* ws, const Tiling& t, cudaStream_t st) {
     float2* part = static_cast<float2*>(ws);
     const IO* x = (const IO*)a.x;
     group_norm_stats_kernel<IO, V><<<tile_ctas(t), kThreads, 0, st>>>(x, part, t);
-    group_norm_apply_kernel<IO, V><<<tile_ctas(t), kThreads, 0, st>>>(
-        x, (const IO*)a.gate, a.gamma, a.beta, a.eps, a.silu, part, (IO*)y, t);
+    group_norm_apply_kernel<IO, V, kGate, kSilu><<<tile_ctas(t), kThreads, 0, st>>>(
+        x, (const IO*)a.gate, a.gamma, a.beta, a.eps, part, (IO*)y, t);
     return cudaGetLastError();
 }
-template <typename IO, int V>
+template <typename IO, int V, bool kGate, bool kSilu>
 cudaError_t positions_bwd(const GroupNorm& a, const void* dy, void* dx, float* dgamma, float* dbeta,
                           void* dgate, void* ws, const Tiling& t, cudaStream_t st) {
     uint8_t* w = static_cast<uint8_t*>(ws);
@@ -921,11 +947,21 @@ cudaError_t positions_bwd(const GroupNorm& a, const void* dy, void* dx, float* d
     const IO *x = (const IO*)a.x, *gate = (const IO*)a.gate, *d = (const IO*)dy;
     const unsigned grid = tile_ctas(t), params = (unsigned)((2 * t.C + 31) / 32);
     group_norm_stats_kernel<IO, V><<<grid, kThreads, 0, st>>>(x, part, t);
-    group_norm_bwd_sums_kernel<IO, V><<<grid, kThreads, 0, st>>>(
-        x, gate, a.gamma, a.beta, a.eps, a.silu, part, d, (IO*)dgate, stats, rows, sums, t);
-    group_norm_bwd_apply_kernel<IO, V><<<grid + params, kThreads, 0, st>>>(
-        x, gate, a.gamma, a.beta, a.silu, stats, sums, d, (IO*)dx, rows, dgamma, dbeta, grid, t);
+    group_norm_bwd_sums_kernel<IO, V, kGate, kSilu><<<grid, kThreads, 0, st>>>(
+        x, gate, a.gamma, a.beta, a.eps, part, d, (IO*)dgate, stats, rows, sums, t);
+    group_norm_bwd_apply_kernel<IO, V, kGate, kSilu><<<grid + params, kThreads, 0, st>>>(
+        x, gate, a.gamma, a.beta, stats, sums, d, (IO*)dx, rows, dgamma, dbeta, grid, t);
     return cudaGetLastError();
+}
+// f(vector width, gate, silu), the three as compile-time constants
+template <typename F>
+cudaError_t with_constants(const GroupNorm& a, const Tiling& t, F f) {
+    using std::integral_constant;
+    auto act = [&](auto v, auto gate) {
+        return a.silu ? f(v, gate, std::true_type{}) : f(v, gate, std::false_type{});
+    };
+    auto gated = [&](auto v) { return a.gate ? act(v, std::true_type{}) : act(v, std::false_type{}); };
+    return t.V == 8 ? gated(integral_constant<int, 8>{}) : gated(integral_constant<int, 1>{});
 }
 
 template <typename IO>
@@ -941,7 +977,9 @@ cudaError_t forward_io(const GroupNorm& a, void* y, void* ws, cudaStream_t st) {
              : rows_fwd<IO, 1, 0>(a, y, s, st);
     }
     const Tiling t = tiling(a.N, a.L, a.C, a.groups);
-    return t.V == 8 ? positions_fwd<IO, 8>(a, y, ws, t, st) : positions_fwd<IO, 1>(a, y, ws, t, st);
+    return with_constants(a, t, [&](auto v, auto gate, auto silu) {
+        return positions_fwd<IO, v(), gate(), silu()>(a, y, ws, t, st);
+    });
 }
 
 template <typename IO>
@@ -968,8 +1006,9 @@ cudaError_t backward_io(const GroupNorm& a, const void* dy, void* dx, float* dga
         return cudaGetLastError();
     }
     const Tiling t = tiling(a.N, a.L, a.C, a.groups);
-    return t.V == 8 ? positions_bwd<IO, 8>(a, dy, dx, dgamma, dbeta, dgate, ws, t, st)
-                    : positions_bwd<IO, 1>(a, dy, dx, dgamma, dbeta, dgate, ws, t, st);
+    return with_constants(a, t, [&](auto v, auto gate, auto silu) {
+        return positions_bwd<IO, v(), gate(), silu()>(a, dy, dx, dgamma, dbeta, dgate, ws, t, st);
+    });
 }
 
 }  // namespace
