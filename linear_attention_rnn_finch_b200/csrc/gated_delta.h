@@ -23,8 +23,21 @@ struct GdrIn {
 cudaError_t launch_gdr_recurrent(const GdrIn& in, const float* s_in, float* s_out, void* y,
                                  bool bf16, cudaStream_t st);
 
-// Chunked on tensor cores, bf16 I/O.  s_out may equal s_in or be null; s_in null: zero.
-cudaError_t launch_gdr_chunked(const GdrIn& in, const float* s_in, float* s_out, void* y, cudaStream_t st);
+// Sequences cut into `count` segments of `blocks` blocks of 64 tokens (count 1: not cut).  ctas:
+// CTAs a head and segment; maps: matrices formed for each segment but one (and one less in
+// all); full, part: us a CTA needs for a block with and without outputs.
+struct GdrSegments {
+    int count, blocks;
+};
+GdrSegments gdr_segments(int B, int T, int H, int ctas, int maps, float full, float part);
+// a, m: [head][last][64][64] fp32.  m[i] += a[i] m[i - 1] upwards, or m[i] += a[i + 1]^T m[i + 1]
+// downwards, 0 <= i < last.
+cudaError_t launch_gdr_join(const float* a, float* m, int heads, int last, bool back, cudaStream_t st);
+
+// Chunked on tensor cores, bf16 I/O.  s_out may equal s_in or be null; s_in null: zero.  ws: at
+// least gdr_chunked_bytes(B, T, H) bytes.
+size_t gdr_chunked_bytes(int B, int T, int H);
+cudaError_t launch_gdr_chunked(const GdrIn& in, const float* s_in, float* s_out, void* y, void* ws, cudaStream_t st);
 
 // One token, the state updated in place (T is ignored).
 cudaError_t launch_gdr_decode(const GdrIn& in, float* state, void* y, bool bf16, cudaStream_t st);

@@ -78,7 +78,7 @@ extern "C" {
 
 size_t gated_delta_prefill_workspace_bytes(int B, int T, int H, int HK, int D, wkv_dtype io) {
     if (B <= 0 || T <= 0 || H <= 0 || check_gdr_sizes(B, T, H, HK, D, io, 1.f) != WKV_OK) return 0;
-    return 0;
+    return io == WKV_BF16 ? goldwkv::gdr_chunked_bytes(B, T, H) : 0;
 }
 
 wkv_status gated_delta_prefill(const void* q, const void* k, const void* v, const void* omega,
@@ -104,7 +104,7 @@ wkv_status gated_delta_prefill(const void* q, const void* k, const void* v, cons
     if (injected("launch")) return WKV_ERR_CUDA;
     if (!tokens) return pass_state(state_out, state_in, sb, st);
     const goldwkv::GdrIn in{q, k, v, omega, beta, scale, B, T, H, HK};
-    if (io == WKV_BF16) return from_cuda(goldwkv::launch_gdr_chunked(in, state_in, state_out, y, st));
+    if (io == WKV_BF16) return from_cuda(goldwkv::launch_gdr_chunked(in, state_in, state_out, y, workspace, st));
     return from_cuda(goldwkv::launch_gdr_recurrent(in, state_in, state_out, y, false, st));
 }
 

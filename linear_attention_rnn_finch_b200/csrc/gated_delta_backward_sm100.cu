@@ -38,6 +38,10 @@ struct Args {
     const float* s_in;
     uint8_t* ws;     // [head][block][S, E, G, dF]
     int blocks;
+    // segments of the sequence (gated_delta_segments.cu): A, then the states and the gradients at
+    // the borders, each [head][count - 1][64][64] fp32
+    GdrSegments seg;
+    float *a, *s, *d;
 };
 
 __device__ __forceinline__ uint32_t turn(uint32_t x) {
@@ -78,11 +82,16 @@ struct ChainSmem {
     uint8_t y[kChainWarps][kTile16];
 };
 
-template <bool kBack>
-__device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh) {
-    const int H = p.in.H, HK = p.in.HK, T = p.in.T, b = bh / H, h = bh - b * H, hk = h / (H / HK);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, blocks = p.blocks;
-    const size_t ko = ((size_t)b * T * HK + hk) * C, vo = ((size_t)b * T * H + h) * C, go = (size_t)b * T * H + h;
+// Segment `seg` of head bh from the state (or gradient) `from` (null: zero; `unit`: the identity,
+// with v = 0).  kStore: what the second launch reads, and dV; otherwise only the final matrix.
+template <bool kBack, bool kStore>
+__device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh, int seg, bool unit, const float* from,
+                                      float* to) {
+    const int H = p.in.H, HK = p.in.HK, b = bh / H, h = bh - b * H, hk = h / (H / HK);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int first = seg * p.seg.blocks, T = p.in.T - first * C, blocks = min(p.seg.blocks, p.blocks - first);
+    const size_t bt = (size_t)b * p.in.T + first * C;
+    const size_t ko = (bt * HK + hk) * C, vo = (bt * H + h) * C, go = bt * H + h;
     const bf16 *q = (const bf16*)p.in.q + ko, *k = (const bf16*)p.in.k + ko;
     const bf16* x = (const bf16*)(kBack ? p.g.dy : p.in.v) + vo;
     const uint32_t sk = ptx::smem_addr(s.k), sx = ptx::smem_addr(s.x), sq = ptx::smem_addr(s.q);
@@ -96,7 +105,7 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh) {
             const uint32_t o = (uint32_t)(m % kStages) * kTileBytes;
             const int t0 = block(m) * C;
             copy_block<kPrepThreads>(sk + o, k, (size_t)HK * C, t0, T, pt);
-            copy_block<kPrepThreads>(sx + o, x, (size_t)H * C, t0, T, pt);
+            copy_block<kPrepThreads>(sx + o, x, (size_t)H * C, t0, unit ? 0 : T, pt);
             if (kBack) copy_block<kPrepThreads>(sq + o, q, (size_t)HK * C, t0, T, pt);
             cp_async_commit();
         };
@@ -123,10 +132,10 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh) {
 
     const int c = 2 * (lane & 3);
     float S[8][4];
-    const float* first = kBack ? p.g.ds_out : p.s_in;
-    load_state(S, first ? first + (size_t)bh * C * C : nullptr, warp, lane);
+    if (unit) unit_state(S, warp, lane);
+    else load_state(S, from, warp, lane);
     bf16* dv = (bf16*)p.g.dv + vo + 16 * warp;
-    uint8_t* ws = p.ws + (size_t)bh * blocks * kBlockBytes + (kBack ? 2 * kMat : 0);
+    uint8_t* ws = p.ws + ((size_t)bh * p.blocks + first) * kBlockBytes + (kBack ? 2 * kMat : 0);
     const uint32_t ab = addr_b(0, 0, 0, lane), abt = addr_bt(0, 0, 0, lane), act = addr_ct(0, 0, 2 * warp, lane);
     __syncthreads();
     __syncthreads();   // the preparation's first turn
@@ -136,7 +145,7 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh) {
         const Prep& pr = s.prep[m & 1];
         const uint32_t pt = ptx::smem_addr(pr.t), pp = ptx::smem_addr(pr.p);
         uint8_t* wb = ws + (size_t)block(m) * kBlockBytes;
-        put_state(wb, S, warp, lane);
+        if (kStore) put_state(wb, S, warp, lane);
 #pragma unroll 1
         for (int i0 = 0; i0 < kSubs; ++i0) {
             const int j = kBack ? kSubs - 1 - i0 : i0, row = kSub * j;
@@ -173,7 +182,7 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) value_minus(f[u], g[u], xv[2 * u], xv[2 * u + 1]);
                 times_t(e, f, pt + j * kTile16, lane);
-                put_rows(wb + kMat, e, j, warp, lane);
+                if (kStore) put_rows(wb + kMat, e, j, warp, lane);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) scale_cols(e[u], make_float2(bt[u].x * te[u].x, bt[u].y * te[u].y));
                 update_state(S, pr.g_end[j], e, kt + abt);
@@ -190,8 +199,9 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh) {
                     scale_cols(f[u], bt[u]);
                 }
                 times_t<true>(e, f, pt + j * kTile16, lane);
-                store_tokens(dv + (size_t)(t0 + row) * H * C, (size_t)H * C, T - t0 - row, e, s.y[warp], lane);
-                put_rows(wb + kMat, e, j, warp, lane);
+                if (kStore)
+                    store_tokens(dv + (size_t)(t0 + row) * H * C, (size_t)H * C, T - t0 - row, e, s.y[warp], lane);
+                if (kStore) put_rows(wb + kMat, e, j, warp, lane);
                 // G^T = g_16 G^T + (scale g dY)^T Q - (g dF)^T K
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
@@ -209,17 +219,47 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh) {
         }
         __syncthreads();
     }
-    if (kBack && p.g.ds_in) store_state(p.g.ds_in + (size_t)bh * C * C, S, warp, lane);
+    if (to) store_state(to, S, warp, lane);
 }
 
+// The chains of a head's segments, the longer ones (backward) first.
 __global__ void __launch_bounds__(kTcThreads, 2)
 gated_delta_bwd_chains_kernel(const __grid_constant__ Args p) {
     extern __shared__ __align__(16) uint8_t raw[];
     ChainSmem& s = tiles::smem_aligned<ChainSmem>(raw);
-    // the longer chain first
-    const int heads = p.in.B * p.in.H;
-    if ((int)blockIdx.x < heads) chain<true>(s, p, blockIdx.x);
-    else chain<false>(s, p, blockIdx.x - heads);
+    const int n = p.seg.count, last = n - 1, half = (int)(gridDim.x >> 1);
+    const bool back = (int)blockIdx.x < half;
+    const int i = back ? blockIdx.x : blockIdx.x - half, bh = i / n, seg = i - bh * n;
+    const size_t at = (size_t)bh * C * C, border = (size_t)bh * last;
+    if (back)
+        chain<true, true>(s, p, bh, seg, false,
+                          seg < last ? p.d + (border + seg) * C * C : p.g.ds_out ? p.g.ds_out + at : nullptr,
+                          seg == 0 && p.g.ds_in ? p.g.ds_in + at : nullptr);
+    else
+        chain<false, true>(s, p, bh, seg, false,
+                           seg > 0 ? p.s + (border + seg - 1) * C * C : p.s_in ? p.s_in + at : nullptr, nullptr);
+}
+
+// B of the segments 0 .. count - 2 (the first from the given state), A of 1 .. count - 2, and B' of
+// 1 .. count - 1 (the last from the given gradient).
+__global__ void __launch_bounds__(kTcThreads, 2)
+gated_delta_bwd_maps_kernel(const __grid_constant__ Args p) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    ChainSmem& s = tiles::smem_aligned<ChainSmem>(raw);
+    const int last = p.seg.count - 1, each = 3 * last - 1, bh = blockIdx.x / each, i = blockIdx.x - bh * each;
+    const size_t at = (size_t)bh * C * C, border = (size_t)bh * last;
+    if (i < last) {
+        const int seg = i + 1;
+        chain<true, false>(s, p, bh, seg, false, seg == last && p.g.ds_out ? p.g.ds_out + at : nullptr,
+                           p.d + (border + i) * C * C);
+    } else if (i < 2 * last) {
+        const int seg = i - last;
+        chain<false, false>(s, p, bh, seg, false, seg == 0 && p.s_in ? p.s_in + at : nullptr,
+                            p.s + (border + seg) * C * C);
+    } else {
+        const int seg = i - 2 * last + 1;
+        chain<false, false>(s, p, bh, seg, true, nullptr, p.a + (border + seg) * C * C);
+    }
 }
 
 // ------------------------------------------------------------------ dQ, dK, dbeta, domega
@@ -624,14 +664,29 @@ cudaError_t run(Kernel kernel, unsigned grid, int threads, size_t smem, const Ar
 
 }  // namespace
 
+static GdrSegments segments(int B, int T, int H) { return gdr_segments(B, T, H, 2, 3, 2.5f, 2.0f); }
+
 size_t gdr_backward_tc_bytes(int B, int T, int H) {
-    return (size_t)B * H * ((T + C - 1) / C) * kBlockBytes;
+    const size_t heads = (size_t)B * H;
+    return heads * ((T + C - 1) / C) * kBlockBytes +
+           3 * sizeof(float) * heads * (segments(B, T, H).count - 1) * C * C;
 }
 
 cudaError_t launch_gdr_backward_tc(const GdrIn& in, const float* s_in, const GdrGrads& g, void* ws, cudaStream_t st) {
-    const Args a{in, g, s_in, static_cast<uint8_t*>(ws), (in.T + C - 1) / C};
-    cudaError_t e = run(gated_delta_bwd_chains_kernel, 2u * (unsigned)(in.B * in.H), kTcThreads,
-                        sizeof(ChainSmem) + 1024, a, st);
+    Args a{in, g, s_in, static_cast<uint8_t*>(ws), (in.T + C - 1) / C, segments(in.B, in.T, in.H), nullptr, nullptr, nullptr};
+    const unsigned heads = (unsigned)(in.B * in.H), last = a.seg.count - 1;
+    const size_t smem = sizeof(ChainSmem) + 1024;
+    cudaError_t e;
+    if (last > 0) {
+        a.a = reinterpret_cast<float*>(a.ws + (size_t)heads * a.blocks * kBlockBytes);
+        a.s = a.a + (size_t)heads * last * C * C;
+        a.d = a.s + (size_t)heads * last * C * C;
+        e = run(gated_delta_bwd_maps_kernel, heads * (3 * last - 1), kTcThreads, smem, a, st);
+        if (e == cudaSuccess) e = launch_gdr_join(a.a, a.s, (int)heads, (int)last, false, st);
+        if (e == cudaSuccess) e = launch_gdr_join(a.a, a.d, (int)heads, (int)last, true, st);
+        if (e != cudaSuccess) return e;
+    }
+    e = run(gated_delta_bwd_chains_kernel, 2u * heads * a.seg.count, kTcThreads, smem, a, st);
     if (e != cudaSuccess) return e;
     return run(gated_delta_bwd_out_tc_kernel, (unsigned)(in.B * in.HK) * (unsigned)a.blocks, kOutThreads,
                sizeof(OutSmem) + 1024, a, st);

@@ -242,6 +242,13 @@ __device__ __forceinline__ void load_state(float (&S)[8][4], const float* src, i
         for (int e = 0; e < 4; ++e)
             S[i][e] = src ? src[(8 * i + c + (e & 1)) * C + 16 * cw + r + 8 * (e >> 1)] : 0.f;
 }
+__device__ __forceinline__ void unit_state(float (&S)[8][4], int cw, int lane) {
+    const int r = lane >> 2, c = 2 * (lane & 3);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[i][e] = 8 * i + c + (e & 1) == 16 * cw + r + 8 * (e >> 1) ? 1.f : 0.f;
+}
 __device__ __forceinline__ void store_state(float* dst, const float (&S)[8][4], int cw, int lane) {
     const int r = lane >> 2, c = 2 * (lane & 3);
 #pragma unroll
