@@ -19,9 +19,9 @@ struct GdrIn {
     int B, T, H, HK;
 };
 
-// Token-by-token recurrence on CUDA cores.  s_out may equal s_in or be null; s_in null: zero.
-cudaError_t launch_gdr_recurrent(const GdrIn& in, const float* s_in, float* s_out, void* y,
-                                 bool bf16, cudaStream_t st);
+// Token-by-token recurrence on CUDA cores, fp32 I/O.  s_out may equal s_in or be null; s_in null:
+// zero.
+cudaError_t launch_gdr_recurrent(const GdrIn& in, const float* s_in, float* s_out, void* y, cudaStream_t st);
 
 // Sequences cut into `count` segments of `blocks` blocks of 64 tokens (count 1: not cut).  ctas:
 // CTAs a head and segment; maps: matrices formed for each segment but one (and one less in
@@ -42,8 +42,8 @@ cudaError_t launch_gdr_chunked(const GdrIn& in, const float* s_in, float* s_out,
 // One token, the state updated in place (T is ignored).
 cudaError_t launch_gdr_decode(const GdrIn& in, float* state, void* y, bool bf16, cudaStream_t st);
 
-// Backward on CUDA cores in fp32, chunk by chunk (either I/O type).  ws: at least
-// gdr_backward_simt_bytes(B, T, H) bytes.
+// Backward on CUDA cores, fp32 I/O, chunk by chunk.  ws: at least gdr_backward_f32_bytes(B, T, H)
+// bytes.
 struct GdrGrads {
     const void* dy;
     const float* ds_out;   // null: zero
@@ -54,9 +54,8 @@ struct GdrGrads {
     void* dbeta;
     float* ds_in;          // null: not written
 };
-size_t gdr_backward_simt_bytes(int B, int T, int H);
-cudaError_t launch_gdr_backward_simt(const GdrIn& in, const float* s_in, const GdrGrads& g,
-                                     void* ws, bool bf16, cudaStream_t st);
+size_t gdr_backward_f32_bytes(int B, int T, int H);
+cudaError_t launch_gdr_backward_f32(const GdrIn& in, const float* s_in, const GdrGrads& g, void* ws, cudaStream_t st);
 
 // Backward on tensor cores, bf16 I/O.  ws: at least gdr_backward_tc_bytes(B, T, H) bytes.
 size_t gdr_backward_tc_bytes(int B, int T, int H);

@@ -105,7 +105,7 @@ wkv_status gated_delta_prefill(const void* q, const void* k, const void* v, cons
     if (!tokens) return pass_state(state_out, state_in, sb, st);
     const goldwkv::GdrIn in{q, k, v, omega, beta, scale, B, T, H, HK};
     if (io == WKV_BF16) return from_cuda(goldwkv::launch_gdr_chunked(in, state_in, state_out, y, workspace, st));
-    return from_cuda(goldwkv::launch_gdr_recurrent(in, state_in, state_out, y, false, st));
+    return from_cuda(goldwkv::launch_gdr_recurrent(in, state_in, state_out, y, st));
 }
 
 wkv_status gated_delta_decode_step(const void* q, const void* k, const void* v, const void* omega,
@@ -129,7 +129,7 @@ wkv_status gated_delta_decode_step(const void* q, const void* k, const void* v, 
 
 size_t gated_delta_backward_workspace_bytes(int B, int T, int H, int HK, int D, wkv_dtype io) {
     if (B <= 0 || T <= 0 || H <= 0 || check_gdr_sizes(B, T, H, HK, D, io, 1.f) != WKV_OK) return 0;
-    return io == WKV_BF16 ? goldwkv::gdr_backward_tc_bytes(B, T, H) : goldwkv::gdr_backward_simt_bytes(B, T, H);
+    return io == WKV_BF16 ? goldwkv::gdr_backward_tc_bytes(B, T, H) : goldwkv::gdr_backward_f32_bytes(B, T, H);
 }
 
 wkv_status gated_delta_backward(const void* q, const void* k, const void* v, const void* omega,
@@ -162,7 +162,7 @@ wkv_status gated_delta_backward(const void* q, const void* k, const void* v, con
     const goldwkv::GdrIn in{q, k, v, omega, beta, scale, B, T, H, HK};
     const goldwkv::GdrGrads g{dy, dstate_out, dq, dk, dv, domega, dbeta, dstate_in};
     if (io == WKV_BF16) return from_cuda(goldwkv::launch_gdr_backward_tc(in, state_in, g, workspace, st));
-    return from_cuda(goldwkv::launch_gdr_backward_simt(in, state_in, g, workspace, false, st));
+    return from_cuda(goldwkv::launch_gdr_backward_f32(in, state_in, g, workspace, st));
 }
 
 size_t group_norm_act_workspace_bytes(long N, long L, int C, int groups, wkv_dtype io) {

@@ -20,12 +20,12 @@
 //              + sum_{s < t} V'_s . (Kt G)_s + g_C <G, S>,
 //     domega_t = -exp(omega_t) dlog w_t.
 //
-// Four launches: what depends on no state, parallel over chunks (T, P^T dY, scale (g Q)^T dY);
-// the states S forward; the gradients G backward, each a chain over a head's chunks of three
-// 64 x 64 x 64 products; and dQ, dK, db, domega, parallel over chunks, a CTA per key head
-// that adds up its value heads in registers (no atomics: the same bits every time).  All
-// products are fp32 FMAs over shared-memory tiles, a thread 4 x 4 of the 64 x 64 results:
-// this is the fp32 path, where the CUDA cores bound it.
+// The fp32 path, where the CUDA cores bound it.  Three launches: what depends on no state,
+// parallel over chunks (T, P^T dY, scale (g Q)^T dY); the states S forward and the gradients G
+// backward, chains over a head's chunks of three 64 x 64 x 64 products each that need nothing
+// of each other, in CTAs of their own; and dQ, dK, db, domega, parallel over chunks, a CTA per
+// key head that adds up its value heads in registers (no atomics: the same bits every time).
+// All products are fp32 FMAs over shared-memory tiles.
 #include "common.cuh"
 #include "gated_delta.h"
 #include "gated_delta_math.cuh"
@@ -36,18 +36,43 @@ namespace {
 
 using namespace gdr;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;                 // 16 warps: a product is 2000 issue cycles a scheduler
+                                              // and half hidden latency with 8
 constexpr int kLd = C + 4;                    // padded row of a shared-memory tile
 constexpr int kTileFloats = C * kLd;
 constexpr size_t kMat = (size_t)C * C;        // floats of one 64 x 64 matrix in the workspace
 
-// Results of a product: rows 4 ty + i, columns 4 tx + j, or tx + 16 j where kStr.
-template <bool kStr>
-__device__ __forceinline__ int col(int tx, int j) { return kStr ? tx + 16 * j : 4 * tx + j; }
+// A thread's results of a product: rows 4 ty + i, kJ columns: kJ tx + j, or strided by 64 / kJ.
+template <int kJ, bool kStr>
+__device__ __forceinline__ int col(int tx, int j) { return kStr ? tx + C / kJ * j : kJ * tx + j; }
 
-// acc += op(A) op(B) over 64 x 64 tiles; B transposed forces the strided columns.
-template <bool kTA, bool kTB, bool kStr>
-__device__ __forceinline__ void mm(float (&acc)[4][4], const float* A, const float* B, int ty, int tx) {
+template <int kJ>
+__device__ __forceinline__ void load_cols(float (&v)[kJ], const float* p) {
+    if (kJ == 1) {
+        v[0] = p[0];
+    } else if (kJ == 2) {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        v[0] = x.x;
+        v[kJ - 1] = x.y;
+    } else {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        v[0] = x.x;
+        v[1 % kJ] = x.y;
+        v[2 % kJ] = x.z;
+        v[3 % kJ] = x.w;
+    }
+}
+template <int kJ>
+__device__ __forceinline__ void store_cols(float* p, const float (&v)[kJ]) {
+    if (kJ == 1) *p = v[0];
+    else if (kJ == 2) *reinterpret_cast<float2*>(p) = make_float2(v[0], v[kJ - 1]);
+    else *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1 % kJ], v[2 % kJ], v[3 % kJ]);
+}
+
+// acc += op(A) op(B), A 64 x 64, B 64 rows of row length ldb (transposed: 64 x 64, which forces
+// the strided columns).
+template <bool kTA, bool kTB, bool kStr, int kJ>
+__device__ __forceinline__ void mm(float (&acc)[4][kJ], const float* A, const float* B, int ty, int tx, int ldb = kLd) {
     static_assert(!kTB || kStr, "a transposed B has strided columns");
     static_assert(!(kTA && kTB), "not needed");
 #pragma unroll 2
@@ -58,82 +83,69 @@ __device__ __forceinline__ void mm(float (&acc)[4][4], const float* A, const flo
             for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * kLd + k);
         }
         if (kTB) {
-            float4 b[4];
+            float4 b[kJ];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * kLd + k);
+            for (int j = 0; j < kJ; ++j) b[j] = *reinterpret_cast<const float4*>(B + (tx + C / kJ * j) * kLd + k);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < kJ; ++j)
                     acc[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, acc[i][j]))));
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float av[4], bv[4];
+                float av[4], bv[kJ];
                 if (kTA) {
-                    const float4 x = *reinterpret_cast<const float4*>(A + (k + e) * kLd + 4 * ty);
-                    av[0] = x.x; av[1] = x.y; av[2] = x.z; av[3] = x.w;
+                    load_cols<4>(av, A + (k + e) * kLd + 4 * ty);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) av[i] = e == 0 ? a[i].x : e == 1 ? a[i].y : e == 2 ? a[i].z : a[i].w;
                 }
                 if (kStr) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) bv[j] = B[(k + e) * kLd + tx + 16 * j];
+                    for (int j = 0; j < kJ; ++j) bv[j] = B[(k + e) * kLd + tx + C / kJ * j];
                 } else {
-                    const float4 x = *reinterpret_cast<const float4*>(B + (k + e) * kLd + 4 * tx);
-                    bv[0] = x.x; bv[1] = x.y; bv[2] = x.z; bv[3] = x.w;
+                    load_cols<kJ>(bv, B + (k + e) * ldb + kJ * tx);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+                    for (int j = 0; j < kJ; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
             }
         }
     }
 }
 
-__device__ __forceinline__ void clear(float (&acc)[4][4]) {
+template <int kJ>
+__device__ __forceinline__ void clear(float (&acc)[4][kJ]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < kJ; ++j) acc[i][j] = 0.f;
 }
 
-// Rows t0 .. t0 + 63 of a token tensor (row stride `step` elements) into a tile, rows at T or
-// beyond as zeros.  A thread moves 16 channels of one row.
-template <typename IO>
-__device__ __forceinline__ void load_tokens(float* tile, const IO* base, size_t step, int t0, int T) {
-    const int r = threadIdx.x >> 2, c = 16 * (threadIdx.x & 3);
+// Rows t0 .. t0 + 63 of a token tensor (row stride `step` values) into a tile, rows at T or
+// beyond as zeros.  A thread moves 8 channels of one row.
+__device__ __forceinline__ void load_tokens(float* tile, const float* base, size_t step, int t0, int T) {
+    const int r = threadIdx.x >> 3, c = 8 * (threadIdx.x & 7);
     float* dst = tile + r * kLd + c;
-    if (t0 + r < T) {
-        const IO* src = base + (size_t)(t0 + r) * step + c;
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(dst + i) = load4(src + i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+    for (int i = 0; i < 8; i += 4)
+        *reinterpret_cast<float4*>(dst + i) =
+            t0 + r < T ? load4(base + (size_t)(t0 + r) * step + c + i) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
-// A 64 x 64 fp32 matrix of the workspace into a tile (null: zeros).
+// A 64 x 64 fp32 matrix of the workspace into a tile.
 __device__ __forceinline__ void load_matrix(float* tile, const float* src) {
-    const int r = threadIdx.x >> 2, c = 16 * (threadIdx.x & 3);
+    const int r = threadIdx.x >> 3, c = 8 * (threadIdx.x & 7);
 #pragma unroll
-    for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<float4*>(tile + r * kLd + c + i) =
-            src ? *reinterpret_cast<const float4*>(src + r * C + c + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < 8; i += 4)
+        *reinterpret_cast<float4*>(tile + r * kLd + c + i) = *reinterpret_cast<const float4*>(src + r * C + c + i);
 }
 __device__ __forceinline__ void store_matrix(float* dst, const float* tile) {
-    const int r = threadIdx.x >> 2, c = 16 * (threadIdx.x & 3);
+    const int r = threadIdx.x >> 3, c = 8 * (threadIdx.x & 7);
 #pragma unroll
-    for (int i = 0; i < 16; i += 4)
+    for (int i = 0; i < 8; i += 4)
         *reinterpret_cast<float4*>(dst + r * C + c + i) = *reinterpret_cast<const float4*>(tile + r * kLd + c + i);
-}
-__device__ __forceinline__ void store_acc(float* tile, const float (&acc)[4][4], int ty, int tx) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4*>(tile + (4 * ty + i) * kLd + 4 * tx) =
-            make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
 }
 
 // T = (I + A)^-1 of the strictly lower triangular tile A: each 16 x 16 diagonal block by
@@ -203,27 +215,26 @@ struct LocalSmem {
     Gates gates;
 };
 
-template <typename IO>
 __global__ void __launch_bounds__(kThreads)
 gated_delta_bwd_local_kernel(Args p) {
     extern __shared__ __align__(16) uint8_t raw[];
     LocalSmem& s = *reinterpret_cast<LocalSmem*>(raw);
     const int n = blockIdx.x % p.NC, bh = blockIdx.x / p.NC;
     const int H = p.in.H, HK = p.in.HK, T = p.in.T, b = bh / H, h = bh - b * H, hk = h / (H / HK);
-    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, t0 = n * C;
-    load_tokens(s.q, (const IO*)p.in.q + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, t0, T);
-    load_tokens(s.k, (const IO*)p.in.k + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, t0, T);
-    load_tokens(s.dy, (const IO*)p.dy + ((size_t)b * T * H + h) * C, (size_t)H * C, t0, T);
-    load_gates(s.gates, (const IO*)p.in.omega, (const IO*)p.in.beta, (size_t)b * T * H + h, H, t0, T);
+    const int tid = threadIdx.x, ty = tid >> 5, tx = tid & 31, t0 = n * C;
+    load_tokens(s.q, (const float*)p.in.q + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, t0, T);
+    load_tokens(s.k, (const float*)p.in.k + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, t0, T);
+    load_tokens(s.dy, (const float*)p.dy + ((size_t)b * T * H + h) * C, (size_t)H * C, t0, T);
+    load_gates(s.gates, (const float*)p.in.omega, (const float*)p.in.beta, (size_t)b * T * H + h, H, t0, T);
     __syncthreads();
-    float acc[4][4];
+    float acc[4][2];
     clear(acc);
-    mm<false, true, true>(acc, s.k, s.k, ty, tx);
+    mm<false, true, true, 2>(acc, s.k, s.k, ty, tx);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int t = 4 * ty + i, u = col<true>(tx, j);
+        for (int j = 0; j < 2; ++j) {
+            const int t = 4 * ty + i, u = col<2, true>(tx, j);
             s.a[t * kLd + u] = t > u ? acc[i][j] * s.gates.between(t, u) * s.gates.beta[u] : 0.f;
         }
     __syncthreads();
@@ -231,169 +242,166 @@ gated_delta_bwd_local_kernel(Args p) {
     const size_t at = ((size_t)bh * p.NC + n) * kMat;
     store_matrix(p.wT + at, s.t);
     clear(acc);
-    mm<false, true, true>(acc, s.q, s.k, ty, tx);
+    mm<false, true, true, 2>(acc, s.q, s.k, ty, tx);
     __syncthreads();   // A's last use was in invert
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int t = 4 * ty + i, u = col<true>(tx, j);
+        for (int j = 0; j < 2; ++j) {
+            const int t = 4 * ty + i, u = col<2, true>(tx, j);
             s.a[t * kLd + u] = t >= u ? p.in.scale * acc[i][j] * s.gates.between(t, u) : 0.f;
         }
     // q <- scale g q
     {
-        const int r = tid >> 2, c = 16 * (tid & 3);
+        const int r = tid >> 3, c = 8 * (tid & 7);
         const float f = p.in.scale * s.gates.g[r];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s.q[r * kLd + c + i] *= f;
+        for (int i = 0; i < 8; ++i) s.q[r * kLd + c + i] *= f;
     }
     __syncthreads();
     clear(acc);
-    mm<true, false, false>(acc, s.a, s.dy, ty, tx);
+    mm<true, false, false, 2>(acc, s.a, s.dy, ty, tx);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4*>(p.wX + at + (4 * ty + i) * C + 4 * tx) =
-            make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        store_cols<2>(p.wX + at + (4 * ty + i) * C + 2 * tx, acc[i]);
     clear(acc);
-    mm<true, false, false>(acc, s.q, s.dy, ty, tx);
+    mm<true, false, false, 2>(acc, s.q, s.dy, ty, tx);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4*>(p.wG + at + (4 * ty + i) * C + 4 * tx) =
-            make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        store_cols<2>(p.wG + at + (4 * ty + i) * C + 2 * tx, acc[i]);
 }
 
-// ---- 2: the states, forward
-struct StateSmem {
-    float k[kTileFloats], s[kTileFloats], f[kTileFloats], t[kTileFloats];
+// ---- 2: the states forward, the state gradients backward and dV
+// A CTA of 256 threads takes kCols value columns of a head, which are independent: all 64 where
+// there are heads enough for the device, else 16, whose chunk takes a quarter of the time (three
+// products, 1000 issue cycles each instead of 3000) for about twice the shared-memory reads in
+// all.  The next chunk's K, T and V are on their way in registers while one is worked on.
+constexpr int kChainThreads = 256;
+template <int kCols>
+struct ChainSmem {
+    static constexpr int kLdc = kCols + 4;
+    float k[kTileFloats], t[kTileFloats];
+    float m[C * kLdc], f[C * kLdc];   // S or G; F, then b to_end E, or b X, then -g dF
     Gates gates;
 };
 
-template <typename IO>
-__global__ void __launch_bounds__(kThreads)
-gated_delta_bwd_states_kernel(Args p) {
-    extern __shared__ __align__(16) uint8_t raw[];
-    StateSmem& s = *reinterpret_cast<StateSmem*>(raw);
-    const int bh = blockIdx.x;
+template <int kCols, bool kBack>
+__device__ __forceinline__ void chain(ChainSmem<kCols>& s, const Args& p, int bh, int cols) {
+    constexpr int kJ = kCols / 16, kLdc = ChainSmem<kCols>::kLdc;
     const int H = p.in.H, HK = p.in.HK, T = p.in.T, b = bh / H, h = bh - b * H, hk = h / (H / HK);
-    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    load_matrix(s.s, p.s_in ? p.s_in + (size_t)bh * kMat : nullptr);
-    for (int n = 0; n < p.NC; ++n) {
-        const size_t at = ((size_t)bh * p.NC + n) * kMat;
-        load_tokens(s.k, (const IO*)p.in.k + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, n * C, T);
-        load_tokens(s.f, (const IO*)p.in.v + ((size_t)b * T * H + h) * C, (size_t)H * C, n * C, T);
-        load_matrix(s.t, p.wT + at);
-        load_gates(s.gates, (const IO*)p.in.omega, (const IO*)p.in.beta, (size_t)b * T * H + h, H, n * C, T);
-        __syncthreads();
-        store_matrix(p.wS + at, s.s);
-        float acc[4][4];
-        clear(acc);
-        mm<false, false, false>(acc, s.k, s.s, ty, tx);
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, c0 = cols + kJ * tx;
+    const float* k = (const float*)p.in.k + ((size_t)b * T * HK + hk) * C;
+    const float* v = (const float*)p.in.v + ((size_t)b * T * H + h) * C + c0;
+    float* dv = (float*)p.dv + ((size_t)b * T * H + h) * C + c0;
+    const size_t head = (size_t)bh * p.NC * kMat;
+
+    // 16 values of a row of K and of T; the thread's own values of V
+    const int lr = tid >> 2, lc = 16 * (tid & 3);
+    float4 rk[4], rt[4];
+    float rv[4][kJ];
+    auto fetch = [&](int n) {
+        const int t = n * C + lr;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+            rk[i] = t < T ? load4(k + (size_t)t * HK * C + lc + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            rt[i] = load4(p.wT + head + n * kMat + lr * C + lc + 4 * i);
+            if (!kBack) {
+                const int tv = n * C + 4 * ty + i;
+                if (tv < T) {
+                    load_cols<kJ>(rv[i], v + (size_t)tv * H * C);
+                } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {   // F = V - g (K S), each element its own thread's
-                float* f = &s.f[(4 * ty + i) * kLd + 4 * tx + j];
-                *f = fmaf(-s.gates.g[4 * ty + i], acc[i][j], *f);
+                    for (int j = 0; j < kJ; ++j) rv[i][j] = 0.f;
+                }
             }
+        }
+    };
+    float m[4][kJ];   // rows 4 ty + i of S or G
+    const float* from = kBack ? p.ds_out : p.s_in;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (from) {
+            load_cols<kJ>(m[i], from + (size_t)bh * kMat + (4 * ty + i) * C + c0);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) m[i][j] = 0.f;
+        }
+    }
+    fetch(kBack ? p.NC - 1 : 0);
+    for (int step = 0; step < p.NC; ++step) {
+        const int n = kBack ? p.NC - 1 - step : step;
+        const size_t at = head + n * kMat;
+        float x[4][kJ], y[4][kJ];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<float4*>(s.k + lr * kLd + lc + 4 * i) = rk[i];
+            *reinterpret_cast<float4*>(s.t + lr * kLd + lc + 4 * i) = rt[i];
+            store_cols<kJ>(s.m + (4 * ty + i) * kLdc + kJ * tx, m[i]);
+            const size_t o = at + (4 * ty + i) * C + c0;
+            if (kBack) {
+                load_cols<kJ>(x[i], p.wX + o);   // P^T dY
+                load_cols<kJ>(y[i], p.wG + o);   // scale (g Q)^T dY, whose place G takes
+                store_cols<kJ>(p.wG + o, m[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) x[i][j] = rv[i][j];
+                store_cols<kJ>(p.wS + o, m[i]);
+            }
+        }
+        load_gates(s.gates, (const float*)p.in.omega, (const float*)p.in.beta, (size_t)b * T * H + h, H, n * C, T);
         __syncthreads();
+        if (step + 1 < p.NC) fetch(kBack ? n - 1 : n + 1);
+        float acc[4][kJ];
         clear(acc);
-        mm<false, false, false>(acc, s.t, s.f, ty, tx);
-        __syncthreads();
+        mm<false, false, false, kJ>(acc, s.k, s.m, ty, tx, kLdc);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = 4 * ty + i;
-            *reinterpret_cast<float4*>(p.wE + at + t * C + 4 * tx) =
-                make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-            const float f = s.gates.beta[t] * s.gates.to_end[t];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] *= f;
+            for (int j = 0; j < kJ; ++j)   // F = V - g (K S), or b X = b (P^T dY + Kt G)
+                acc[i][j] = kBack ? s.gates.beta[t] * fmaf(s.gates.to_end[t], acc[i][j], x[i][j])
+                                  : fmaf(-s.gates.g[t], acc[i][j], x[i][j]);
+            store_cols<kJ>(s.f + t * kLdc + kJ * tx, acc[i]);
         }
-        store_acc(s.f, acc, ty, tx);
+        __syncthreads();
+        clear(acc);
+        mm<kBack, false, false, kJ>(acc, s.t, s.f, ty, tx, kLdc);   // E = T F, or dF = T^T (b X)
         __syncthreads();
         const float gc = s.gates.g[C - 1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float4 x = *reinterpret_cast<const float4*>(&s.s[(4 * ty + i) * kLd + 4 * tx]);
-            acc[i][0] = gc * x.x;
-            acc[i][1] = gc * x.y;
-            acc[i][2] = gc * x.z;
-            acc[i][3] = gc * x.w;
+            const int t = 4 * ty + i;
+            store_cols<kJ>((kBack ? p.wX : p.wE) + at + t * C + c0, acc[i]);
+            if (kBack && n * C + t < T) store_cols<kJ>(dv + (size_t)(n * C + t) * H * C, acc[i]);
+            const float f = kBack ? -s.gates.g[t] : s.gates.beta[t] * s.gates.to_end[t];
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+                acc[i][j] *= f;
+                m[i][j] = kBack ? fmaf(gc, m[i][j], y[i][j]) : gc * m[i][j];
+            }
+            store_cols<kJ>(s.f + t * kLdc + kJ * tx, acc[i]);
         }
-        mm<true, false, false>(acc, s.k, s.f, ty, tx);
-        store_acc(s.s, acc, ty, tx);
+        __syncthreads();
+        mm<true, false, false, kJ>(m, s.k, s.f, ty, tx, kLdc);
         __syncthreads();
     }
+    if (kBack && p.ds_in)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store_cols<kJ>(p.ds_in + (size_t)bh * kMat + (4 * ty + i) * C + c0, m[i]);
 }
 
-// ---- 3: the state gradients, backward; dV
-struct GradStateSmem {
-    float k[kTileFloats], g[kTileFloats], x[kTileFloats], t[kTileFloats];
-    Gates gates;
-};
-
-template <typename IO>
-__global__ void __launch_bounds__(kThreads)
-gated_delta_bwd_state_grads_kernel(Args p) {
+template <int kCols>
+__global__ void __launch_bounds__(kChainThreads)
+gated_delta_bwd_chains_f32_kernel(Args p) {
     extern __shared__ __align__(16) uint8_t raw[];
-    GradStateSmem& s = *reinterpret_cast<GradStateSmem*>(raw);
-    const int bh = blockIdx.x;
-    const int H = p.in.H, HK = p.in.HK, T = p.in.T, b = bh / H, h = bh - b * H, hk = h / (H / HK);
-    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    IO* dv = (IO*)p.dv + ((size_t)b * T * H + h) * C;
-    load_matrix(s.g, p.ds_out ? p.ds_out + (size_t)bh * kMat : nullptr);
-    for (int n = p.NC - 1; n >= 0; --n) {
-        const size_t at = ((size_t)bh * p.NC + n) * kMat;
-        load_tokens(s.k, (const IO*)p.in.k + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, n * C, T);
-        load_matrix(s.t, p.wT + at);
-        load_gates(s.gates, (const IO*)p.in.omega, (const IO*)p.in.beta, (size_t)b * T * H + h, H, n * C, T);
-        __syncthreads();
-        float acc[4][4], into[4][4];
-        clear(acc);
-        mm<false, false, false>(acc, s.k, s.g, ty, tx);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {   // b X = b (P^T dY + Kt G)
-            const int t = 4 * ty + i;
-            const float4 x = *reinterpret_cast<const float4*>(p.wX + at + t * C + 4 * tx);
-            const float e = s.gates.to_end[t], bt = s.gates.beta[t];
-            acc[i][0] = bt * fmaf(e, acc[i][0], x.x);
-            acc[i][1] = bt * fmaf(e, acc[i][1], x.y);
-            acc[i][2] = bt * fmaf(e, acc[i][2], x.z);
-            acc[i][3] = bt * fmaf(e, acc[i][3], x.w);
-            // scale (g Q)^T dY, whose place G takes
-            float4* gp = reinterpret_cast<float4*>(p.wG + at + t * C + 4 * tx);
-            const float4 y = *gp;
-            const float4 G = *reinterpret_cast<const float4*>(&s.g[t * kLd + 4 * tx]);
-            *gp = G;
-            const float gc = s.gates.g[C - 1];
-            into[i][0] = fmaf(gc, G.x, y.x);
-            into[i][1] = fmaf(gc, G.y, y.y);
-            into[i][2] = fmaf(gc, G.z, y.z);
-            into[i][3] = fmaf(gc, G.w, y.w);
-        }
-        store_acc(s.x, acc, ty, tx);
-        __syncthreads();
-        clear(acc);
-        mm<true, false, false>(acc, s.t, s.x, ty, tx);
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = 4 * ty + i;
-            *reinterpret_cast<float4*>(p.wX + at + t * C + 4 * tx) =
-                make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-            if (n * C + t < T) store4(dv + (size_t)(n * C + t) * H * C + 4 * tx, acc[i]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] *= -s.gates.g[t];
-        }
-        store_acc(s.x, acc, ty, tx);
-        __syncthreads();
-        mm<true, false, false>(into, s.k, s.x, ty, tx);
-        store_acc(s.g, into, ty, tx);
-        __syncthreads();
-    }
-    if (p.ds_in) store_matrix(p.ds_in + (size_t)bh * kMat, s.g);
+    ChainSmem<kCols>& s = *reinterpret_cast<ChainSmem<kCols>*>(raw);
+    constexpr int kParts = C / kCols;
+    const int i = blockIdx.x >> 1, bh = i / kParts, cols = kCols * (i - bh * kParts);
+    if (blockIdx.x & 1) chain<kCols, false>(s, p, bh, cols);
+    else chain<kCols, true>(s, p, bh, cols);
 }
 
-// ---- 4: dQ, dK, dbeta, domega
+// ---- 3: dQ, dK, dbeta, domega
 struct OutSmem {
     float q[kTileFloats], k[kTileFloats], dy[kTileFloats], e[kTileFloats], df[kTileFloats];
     float s[kTileFloats], g[kTileFloats], dp[kTileFloats], dm[kTileFloats], w[kTileFloats];
@@ -403,39 +411,38 @@ struct OutSmem {
     Gates gates;
 };
 
-template <typename IO>
 __global__ void __launch_bounds__(kThreads)
 gated_delta_bwd_out_kernel(Args p) {
     extern __shared__ __align__(16) uint8_t raw[];
     OutSmem& s = *reinterpret_cast<OutSmem*>(raw);
     const int n = blockIdx.x % p.NC, bk = blockIdx.x / p.NC;
     const int H = p.in.H, HK = p.in.HK, T = p.in.T, b = bk / HK, hk = bk - b * HK, per = H / HK;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ty = tid >> 4, tx = tid & 15;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ty = tid >> 5, tx = tid & 31;
     const int t0 = n * C;
-    load_tokens(s.q, (const IO*)p.in.q + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, t0, T);
-    load_tokens(s.k, (const IO*)p.in.k + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, t0, T);
-    float dq[4][4], dk[4][4];
+    load_tokens(s.q, (const float*)p.in.q + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, t0, T);
+    load_tokens(s.k, (const float*)p.in.k + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, t0, T);
+    float dq[4][2], dk[4][2];
     clear(dq);
     clear(dk);
     for (int h = hk * per; h < (hk + 1) * per; ++h) {
         const size_t at = ((size_t)(b * H + h) * p.NC + n) * kMat;
-        load_tokens(s.dy, (const IO*)p.dy + ((size_t)b * T * H + h) * C, (size_t)H * C, t0, T);
+        load_tokens(s.dy, (const float*)p.dy + ((size_t)b * T * H + h) * C, (size_t)H * C, t0, T);
         load_matrix(s.e, p.wE + at);
         load_matrix(s.df, p.wX + at);
         load_matrix(s.s, p.wS + at);
         load_matrix(s.g, p.wG + at);
-        load_gates(s.gates, (const IO*)p.in.omega, (const IO*)p.in.beta, (size_t)b * T * H + h, H, t0, T);
+        load_gates(s.gates, (const float*)p.in.omega, (const float*)p.in.beta, (size_t)b * T * H + h, H, t0, T);
         __syncthreads();
-        float acc[4][4], bcc[4][4], w[4][4], cs[4] = {0.f, 0.f, 0.f, 0.f};
+        float acc[4][2], bcc[4][2], w[4][2], cs[2] = {0.f, 0.f};
         clear(acc);
         clear(bcc);
-        mm<false, true, true>(acc, s.q, s.k, ty, tx);
-        mm<false, true, true>(bcc, s.dy, s.e, ty, tx);
+        mm<false, true, true, 2>(acc, s.q, s.k, ty, tx);
+        mm<false, true, true, 2>(bcc, s.dy, s.e, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = 4 * ty + i, u = col<true>(tx, j);
+            for (int j = 0; j < 2; ++j) {
+                const int t = 4 * ty + i, u = col<2, true>(tx, j);
                 const float d = t >= u ? p.in.scale * s.gates.between(t, u) : 0.f;
                 const float x = t >= u ? bcc[i][j] * d * acc[i][j] : 0.f;   // P_ts dY_t . E_s
                 cs[j] += x;
@@ -444,13 +451,13 @@ gated_delta_bwd_out_kernel(Args p) {
             }
         clear(acc);
         clear(bcc);
-        mm<false, true, true>(acc, s.k, s.k, ty, tx);
-        mm<false, true, true>(bcc, s.df, s.e, ty, tx);
+        mm<false, true, true, 2>(acc, s.k, s.k, ty, tx);
+        mm<false, true, true, 2>(bcc, s.df, s.e, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = 4 * ty + i, u = col<true>(tx, j);
+            for (int j = 0; j < 2; ++j) {
+                const int t = 4 * ty + i, u = col<2, true>(tx, j);
                 const float d = t > u ? s.gates.between(t, u) : 0.f;
                 const float x = t > u ? bcc[i][j] * d * acc[i][j] : 0.f;    // M_ts dF_t . E_s
                 cs[j] -= x;
@@ -460,7 +467,7 @@ gated_delta_bwd_out_kernel(Args p) {
                 if (t > u) s.dm[u * kLd + t] = m;
             }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s.cols[ty][col<true>(tx, j)] = cs[j];
+        for (int j = 0; j < 2; ++j) s.cols[ty][col<2, true>(tx, j)] = cs[j];
         // <G, S>
         float gs = 0.f;
         for (int i = tid; i < C * C; i += kThreads) {
@@ -470,11 +477,11 @@ gated_delta_bwd_out_kernel(Args p) {
         gs = warp_sum(gs);
         if (lane == 0) s.red[warp] = gs;
         __syncthreads();
-        mm<false, false, true>(dq, s.dp, s.k, ty, tx);
-        mm<true, false, true>(dk, s.dp, s.q, ty, tx);
-        mm<false, false, true>(dk, s.dm, s.k, ty, tx);
+        mm<false, false, true, 2>(dq, s.dp, s.k, ty, tx);
+        mm<true, false, true, 2>(dk, s.dp, s.q, ty, tx);
+        mm<false, false, true, 2>(dk, s.dm, s.k, ty, tx);
         clear(acc);
-        mm<false, true, true>(acc, s.dy, s.s, ty, tx);
+        mm<false, true, true, 2>(acc, s.dy, s.s, ty, tx);
         float rd[4], ke[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -482,43 +489,43 @@ gated_delta_bwd_out_kernel(Args p) {
             const float f = p.in.scale * s.gates.g[t];
             rd[i] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 const float x = f * acc[i][j];
                 dq[i][j] += x;
-                rd[i] = fmaf(s.q[t * kLd + col<true>(tx, j)], x, rd[i]);
+                rd[i] = fmaf(s.q[t * kLd + col<2, true>(tx, j)], x, rd[i]);
             }
         }
         clear(acc);
-        mm<false, true, true>(acc, s.df, s.s, ty, tx);
+        mm<false, true, true, 2>(acc, s.df, s.s, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = 4 * ty + i;
             const float f = s.gates.g[t];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 const float x = f * acc[i][j];
                 dk[i][j] -= x;
-                rd[i] = fmaf(-s.k[t * kLd + col<true>(tx, j)], x, rd[i]);
+                rd[i] = fmaf(-s.k[t * kLd + col<2, true>(tx, j)], x, rd[i]);
             }
         }
         clear(acc);
-        mm<false, true, true>(acc, s.e, s.g, ty, tx);
+        mm<false, true, true, 2>(acc, s.e, s.g, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = 4 * ty + i;
             const float f = s.gates.to_end[t];
             ke[i] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 const float x = f * acc[i][j];
                 dk[i][j] = fmaf(s.gates.beta[t], x, dk[i][j]);
-                ke[i] = fmaf(s.k[t * kLd + col<true>(tx, j)], x, ke[i]);
+                ke[i] = fmaf(s.k[t * kLd + col<2, true>(tx, j)], x, ke[i]);
             }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) {
+            for (int o = 16; o > 0; o >>= 1) {
                 rd[i] += __shfl_xor_sync(0xffffffffu, rd[i], o);
                 ke[i] += __shfl_xor_sync(0xffffffffu, ke[i], o);
             }
@@ -547,58 +554,57 @@ gated_delta_bwd_out_kernel(Args p) {
             for (int i = 0; i < kThreads / 32; ++i) gsum += s.red[i];
             const float dl = ((pairs + rs) + src) + s.gates.g[C - 1] * gsum;
             const size_t o = (size_t)b * T * H + h + (size_t)(t0 + t) * H;
-            ((IO*)p.domega)[o] = from_f32<IO>(-s.gates.rate[t] * dl);
-            ((IO*)p.dbeta)[o] = from_f32<IO>(db);
+            ((float*)p.domega)[o] = -s.gates.rate[t] * dl;
+            ((float*)p.dbeta)[o] = db;
         }
         __syncthreads();
     }
-    IO* oq = (IO*)p.dq + ((size_t)b * T * HK + hk) * C;
-    IO* ok = (IO*)p.dk + ((size_t)b * T * HK + hk) * C;
+    float* oq = (float*)p.dq + ((size_t)b * T * HK + hk) * C;
+    float* ok = (float*)p.dk + ((size_t)b * T * HK + hk) * C;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = t0 + 4 * ty + i;
         if (t >= T) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            oq[(size_t)t * HK * C + col<true>(tx, j)] = from_f32<IO>(dq[i][j]);
-            ok[(size_t)t * HK * C + col<true>(tx, j)] = from_f32<IO>(dk[i][j]);
+        for (int j = 0; j < 2; ++j) {
+            oq[(size_t)t * HK * C + col<2, true>(tx, j)] = dq[i][j];
+            ok[(size_t)t * HK * C + col<2, true>(tx, j)] = dk[i][j];
         }
     }
 }
 
 template <typename Kernel>
-cudaError_t run(Kernel kernel, unsigned grid, size_t smem, const Args& a, cudaStream_t st) {
+cudaError_t run(Kernel kernel, unsigned grid, int threads, size_t smem, const Args& a, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, smem, st>>>(a);
+    kernel<<<grid, threads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
-template <typename IO>
-cudaError_t backward_io(const Args& a, cudaStream_t st) {
-    const unsigned heads = (unsigned)(a.in.B * a.in.H), chunks = heads * (unsigned)a.NC;
-    cudaError_t e = run(gated_delta_bwd_local_kernel<IO>, chunks, sizeof(LocalSmem), a, st);
-    if (e == cudaSuccess) e = run(gated_delta_bwd_states_kernel<IO>, heads, sizeof(StateSmem), a, st);
-    if (e == cudaSuccess) e = run(gated_delta_bwd_state_grads_kernel<IO>, heads, sizeof(GradStateSmem), a, st);
-    if (e == cudaSuccess)
-        e = run(gated_delta_bwd_out_kernel<IO>, (unsigned)(a.in.B * a.in.HK) * (unsigned)a.NC, sizeof(OutSmem), a, st);
-    return e;
-}
+constexpr int kSms = 148;
 
 }  // namespace
 
-size_t gdr_backward_simt_bytes(int B, int T, int H) {
+size_t gdr_backward_f32_bytes(int B, int T, int H) {
     return 5 * (size_t)B * H * ((T + C - 1) / C) * kMat * sizeof(float);
 }
 
-cudaError_t launch_gdr_backward_simt(const GdrIn& in, const float* s_in, const GdrGrads& g,
-                                     void* ws, bool bf16, cudaStream_t st) {
+cudaError_t launch_gdr_backward_f32(const GdrIn& in, const float* s_in, const GdrGrads& g,
+                                    void* ws, cudaStream_t st) {
     const int NC = (in.T + C - 1) / C;
     const size_t each = (size_t)in.B * in.H * NC * kMat;
     float* w = static_cast<float*>(ws);
     const Args a{in, g.dy, s_in, g.ds_out, g.ds_in, g.dq, g.dk, g.dv, g.domega, g.dbeta,
                  w, w + each, w + 2 * each, w + 3 * each, w + 4 * each, NC};
-    return bf16 ? backward_io<__nv_bfloat16>(a, st) : backward_io<float>(a, st);
+    const unsigned heads = (unsigned)(in.B * in.H);
+    cudaError_t e = run(gated_delta_bwd_local_kernel, heads * NC, kThreads, sizeof(LocalSmem), a, st);
+    if (e != cudaSuccess) return e;
+    if (2 * heads >= (unsigned)kSms)
+        e = run(gated_delta_bwd_chains_f32_kernel<64>, 2 * heads, kChainThreads, sizeof(ChainSmem<64>), a, st);
+    else
+        e = run(gated_delta_bwd_chains_f32_kernel<16>, 8 * heads, kChainThreads, sizeof(ChainSmem<16>), a, st);
+    if (e != cudaSuccess) return e;
+    return run(gated_delta_bwd_out_kernel, (unsigned)(in.B * in.HK) * (unsigned)NC, kThreads, sizeof(OutSmem), a, st);
 }
 
 }  // namespace goldwkv

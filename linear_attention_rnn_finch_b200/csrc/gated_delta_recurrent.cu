@@ -40,12 +40,11 @@ struct Stage {
     float w[kTile], b[kTile], kq[kTile];
 };
 
-template <typename IO>
 __global__ void __launch_bounds__(kThreads)
-gated_delta_recurrent_kernel(const IO* __restrict__ q, const IO* __restrict__ k,
-                             const IO* __restrict__ v, const IO* __restrict__ omega,
-                             const IO* __restrict__ beta, float scale, const float* s_in,
-                             float* s_out, IO* __restrict__ y, int T, int H, int HK) {
+gated_delta_recurrent_kernel(const float* __restrict__ q, const float* __restrict__ k,
+                             const float* __restrict__ v, const float* __restrict__ omega,
+                             const float* __restrict__ beta, float scale, const float* s_in,
+                             float* s_out, float* __restrict__ y, int T, int H, int HK) {
     __shared__ __align__(16) Stage stage[2];
     const int bh = blockIdx.x, b = bh / H, h = bh - b * H, hk = h / (H / HK);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -53,12 +52,12 @@ gated_delta_recurrent_kernel(const IO* __restrict__ q, const IO* __restrict__ k,
     const int jl = warp * 8 + (lane >> 2);        // column within the CTA
     const int j0 = blockIdx.y * kCols;
 
-    const IO* qp = q + ((size_t)b * T * HK + hk) * D;     // token t: + t * HK * D
-    const IO* kp = k + ((size_t)b * T * HK + hk) * D;
-    const IO* vp = v + ((size_t)b * T * H + h) * D + j0;  // token t: + t * H * D
-    const IO* op = omega + (size_t)b * T * H + h;
-    const IO* bp = beta + (size_t)b * T * H + h;
-    IO* yp = y + ((size_t)b * T * H + h) * D + j0 + jl;
+    const float* qp = q + ((size_t)b * T * HK + hk) * D;     // token t: + t * HK * D
+    const float* kp = k + ((size_t)b * T * HK + hk) * D;
+    const float* vp = v + ((size_t)b * T * H + h) * D + j0;  // token t: + t * H * D
+    const float* op = omega + (size_t)b * T * H + h;
+    const float* bp = beta + (size_t)b * T * H + h;
+    float* yp = y + ((size_t)b * T * H + h) * D + j0 + jl;
     const size_t kstep = (size_t)HK * D, vstep = (size_t)H * D;
 
     float S[16];
@@ -133,7 +132,7 @@ gated_delta_recurrent_kernel(const IO* __restrict__ q, const IO* __restrict__ k,
                 S[4 * m + 3] = fmaf(kk[m].w, be, w * S[4 * m + 3]);
             }
             if (part == 0)
-                yp[(size_t)(n * kTile + t) * vstep] = from_f32<IO>(scale * fmaf(s.kq[t], be, w * cs));
+                yp[(size_t)(n * kTile + t) * vstep] = scale * fmaf(s.kq[t], be, w * cs);
         }
     }
     if (s_out) {
@@ -251,14 +250,6 @@ gated_delta_decode_kernel(const IO* __restrict__ q, const IO* __restrict__ k,
 }
 
 template <typename IO>
-cudaError_t recurrent_io(const GdrIn& in, const float* s_in, float* s_out, void* y, cudaStream_t st) {
-    gated_delta_recurrent_kernel<IO><<<dim3((unsigned)(in.B * in.H), D / kCols), kThreads, 0, st>>>(
-        (const IO*)in.q, (const IO*)in.k, (const IO*)in.v, (const IO*)in.omega, (const IO*)in.beta,
-        in.scale, s_in, s_out, (IO*)y, in.T, in.H, in.HK);
-    return cudaGetLastError();
-}
-
-template <typename IO>
 cudaError_t decode_io(const GdrIn& in, float* state, void* y, cudaStream_t st) {
     gated_delta_decode_kernel<IO><<<(unsigned)(in.B * in.H), kDecThreads, 0, st>>>(
         (const IO*)in.q, (const IO*)in.k, (const IO*)in.v, (const IO*)in.omega, (const IO*)in.beta,
@@ -268,10 +259,11 @@ cudaError_t decode_io(const GdrIn& in, float* state, void* y, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_gdr_recurrent(const GdrIn& in, const float* s_in, float* s_out, void* y,
-                                 bool bf16, cudaStream_t st) {
-    return bf16 ? recurrent_io<__nv_bfloat16>(in, s_in, s_out, y, st)
-                : recurrent_io<float>(in, s_in, s_out, y, st);
+cudaError_t launch_gdr_recurrent(const GdrIn& in, const float* s_in, float* s_out, void* y, cudaStream_t st) {
+    gated_delta_recurrent_kernel<<<dim3((unsigned)(in.B * in.H), D / kCols), kThreads, 0, st>>>(
+        (const float*)in.q, (const float*)in.k, (const float*)in.v, (const float*)in.omega,
+        (const float*)in.beta, in.scale, s_in, s_out, (float*)y, in.T, in.H, in.HK);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_gdr_decode(const GdrIn& in, float* state, void* y, bool bf16, cudaStream_t st) {
