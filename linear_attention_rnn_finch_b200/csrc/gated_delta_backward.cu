@@ -36,8 +36,7 @@ namespace {
 
 using namespace gdr;
 
-constexpr int kThreads = 512;                 // 16 warps: a product is 2000 issue cycles a scheduler
-                                              // and half hidden latency with 8
+constexpr int kThreads = 256;
 constexpr int kLd = C + 4;                    // padded row of a shared-memory tile
 constexpr int kTileFloats = C * kLd;
 constexpr size_t kMat = (size_t)C * C;        // floats of one 64 x 64 matrix in the workspace
@@ -70,49 +69,60 @@ __device__ __forceinline__ void store_cols(float* p, const float (&v)[kJ]) {
 }
 
 // acc += op(A) op(B), A 64 x 64, B 64 rows of row length ldb (transposed: 64 x 64, which forces
-// the strided columns).
+// the strided columns).  Four k at a time, the next four's operands read before these are used:
+// with two warps a scheduler nothing else hides shared memory's latency.
 template <bool kTA, bool kTB, bool kStr, int kJ>
 __device__ __forceinline__ void mm(float (&acc)[4][kJ], const float* A, const float* B, int ty, int tx, int ldb = kLd) {
     static_assert(!kTB || kStr, "a transposed B has strided columns");
     static_assert(!(kTA && kTB), "not needed");
-#pragma unroll 2
-    for (int k = 0; k < C; k += 4) {
-        float4 a[4];
-        if (!kTA) {
+    // a[i][e], b[j][e]: k + e
+    auto load = [&](int k, float (&a)[4][4], float (&b)[kJ][4]) {
+        if (kTA) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * kLd + k);
+            for (int e = 0; e < 4; ++e) {
+                float v[4];
+                load_cols<4>(v, A + (k + e) * kLd + 4 * ty);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i][e] = v[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) load_cols<4>(a[i], A + (4 * ty + i) * kLd + k);
         }
         if (kTB) {
-            float4 b[kJ];
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) b[j] = *reinterpret_cast<const float4*>(B + (tx + C / kJ * j) * kLd + k);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < kJ; ++j)
-                    acc[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, acc[i][j]))));
+            for (int j = 0; j < kJ; ++j) load_cols<4>(b[j], B + (tx + C / kJ * j) * kLd + k);
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float av[4], bv[kJ];
-                if (kTA) {
-                    load_cols<4>(av, A + (k + e) * kLd + 4 * ty);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) av[i] = e == 0 ? a[i].x : e == 1 ? a[i].y : e == 2 ? a[i].z : a[i].w;
-                }
+                float v[kJ];
                 if (kStr) {
 #pragma unroll
-                    for (int j = 0; j < kJ; ++j) bv[j] = B[(k + e) * kLd + tx + C / kJ * j];
+                    for (int j = 0; j < kJ; ++j) v[j] = B[(k + e) * kLd + tx + C / kJ * j];
                 } else {
-                    load_cols<kJ>(bv, B + (k + e) * ldb + kJ * tx);
+                    load_cols<kJ>(v, B + (k + e) * ldb + kJ * tx);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < kJ; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+                for (int j = 0; j < kJ; ++j) b[j][e] = v[j];
             }
         }
+    };
+    auto use = [&](const float (&a)[4][4], const float (&b)[kJ][4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) acc[i][j] = fmaf(a[i][e], b[j][e], acc[i][j]);
+    };
+    float a0[4][4], b0[kJ][4], a1[4][4], b1[kJ][4];
+    load(0, a0, b0);
+#pragma unroll 1
+    for (int k = 0; k < C; k += 8) {
+        load(k + 4, a1, b1);
+        use(a0, b0);
+        if (k + 8 < C) load(k + 8, a0, b0);
+        use(a1, b1);
     }
 }
 
@@ -125,26 +135,26 @@ __device__ __forceinline__ void clear(float (&acc)[4][kJ]) {
 }
 
 // Rows t0 .. t0 + 63 of a token tensor (row stride `step` values) into a tile, rows at T or
-// beyond as zeros.  A thread moves 8 channels of one row.
+// beyond as zeros.  A thread moves 16 channels of one row.
 __device__ __forceinline__ void load_tokens(float* tile, const float* base, size_t step, int t0, int T) {
-    const int r = threadIdx.x >> 3, c = 8 * (threadIdx.x & 7);
+    const int r = threadIdx.x >> 2, c = 16 * (threadIdx.x & 3);
     float* dst = tile + r * kLd + c;
 #pragma unroll
-    for (int i = 0; i < 8; i += 4)
+    for (int i = 0; i < 16; i += 4)
         *reinterpret_cast<float4*>(dst + i) =
             t0 + r < T ? load4(base + (size_t)(t0 + r) * step + c + i) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 // A 64 x 64 fp32 matrix of the workspace into a tile.
 __device__ __forceinline__ void load_matrix(float* tile, const float* src) {
-    const int r = threadIdx.x >> 3, c = 8 * (threadIdx.x & 7);
+    const int r = threadIdx.x >> 2, c = 16 * (threadIdx.x & 3);
 #pragma unroll
-    for (int i = 0; i < 8; i += 4)
+    for (int i = 0; i < 16; i += 4)
         *reinterpret_cast<float4*>(tile + r * kLd + c + i) = *reinterpret_cast<const float4*>(src + r * C + c + i);
 }
 __device__ __forceinline__ void store_matrix(float* dst, const float* tile) {
-    const int r = threadIdx.x >> 3, c = 8 * (threadIdx.x & 7);
+    const int r = threadIdx.x >> 2, c = 16 * (threadIdx.x & 3);
 #pragma unroll
-    for (int i = 0; i < 8; i += 4)
+    for (int i = 0; i < 16; i += 4)
         *reinterpret_cast<float4*>(dst + r * C + c + i) = *reinterpret_cast<const float4*>(tile + r * kLd + c + i);
 }
 
@@ -169,21 +179,45 @@ __device__ void invert(float* T, const float* A, float* tmp) {
         }
     }
     __syncthreads();
+    // two results of two rows a thread, four k at a time
+    auto product = [&](const float* X, int ldx, const float* Y, int ldy, int m, int r, int c, float (&v)[2][2]) {
+        v[0][0] = v[0][1] = v[1][0] = v[1][1] = 0.f;
+#pragma unroll 2
+        for (int k = 0; k < m; k += 4) {
+            float x0[4], x1[4];
+            load_cols<4>(x0, X + r * ldx + k);
+            load_cols<4>(x1, X + (r + 1) * ldx + k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float y[2];
+                load_cols<2>(y, Y + (k + e) * ldy + c);
+                v[0][0] = fmaf(x0[e], y[0], v[0][0]);
+                v[0][1] = fmaf(x0[e], y[1], v[0][1]);
+                v[1][0] = fmaf(x1[e], y[0], v[1][0]);
+                v[1][1] = fmaf(x1[e], y[1], v[1][1]);
+            }
+        }
+    };
 #pragma unroll
     for (int m = 16; m < C; m *= 2) {
-        const int blocks = C / (2 * m), n = blocks * m * m;
-        for (int i = tid; i < n; i += kThreads) {
-            const int blk = i / (m * m), r = (i / m) % m, c = i % m, o = 2 * m * blk;
-            float v = 0.f;
-            for (int k = 0; k < m; ++k) v = fmaf(A[(o + m + r) * kLd + o + k], T[(o + k) * kLd + o + c], v);
-            tmp[i] = v;
+        const int quads = m * m / 4, blk = tid / quads, q = tid - blk * quads, o = 2 * m * blk;
+        const int r = 2 * (q / (m / 2)), c = 2 * (q % (m / 2));
+        const bool on = blk < C / (2 * m);
+        float v[2][2];
+        float* t = tmp + blk * m * m;
+        if (on) {
+            product(A + (o + m) * kLd + o, kLd, T + o * kLd + o, kLd, m, r, c, v);
+            store_cols<2>(t + r * m + c, v[0]);
+            store_cols<2>(t + (r + 1) * m + c, v[1]);
         }
         __syncthreads();
-        for (int i = tid; i < n; i += kThreads) {
-            const int blk = i / (m * m), r = (i / m) % m, c = i % m, o = 2 * m * blk;
-            float v = 0.f;
-            for (int k = 0; k < m; ++k) v = fmaf(T[(o + m + r) * kLd + o + m + k], tmp[blk * m * m + k * m + c], v);
-            T[(o + m + r) * kLd + o + c] = -v;
+        if (on) {
+            product(T + (o + m) * kLd + o + m, kLd, t, m, m, r, c, v);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float w[2] = {-v[i][0], -v[i][1]};
+                store_cols<2>(T + (o + m + r + i) * kLd + o + c, w);
+            }
         }
         __syncthreads();
     }
@@ -221,20 +255,20 @@ gated_delta_bwd_local_kernel(Args p) {
     LocalSmem& s = *reinterpret_cast<LocalSmem*>(raw);
     const int n = blockIdx.x % p.NC, bh = blockIdx.x / p.NC;
     const int H = p.in.H, HK = p.in.HK, T = p.in.T, b = bh / H, h = bh - b * H, hk = h / (H / HK);
-    const int tid = threadIdx.x, ty = tid >> 5, tx = tid & 31, t0 = n * C;
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, t0 = n * C;
     load_tokens(s.q, (const float*)p.in.q + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, t0, T);
     load_tokens(s.k, (const float*)p.in.k + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, t0, T);
     load_tokens(s.dy, (const float*)p.dy + ((size_t)b * T * H + h) * C, (size_t)H * C, t0, T);
     load_gates(s.gates, (const float*)p.in.omega, (const float*)p.in.beta, (size_t)b * T * H + h, H, t0, T);
     __syncthreads();
-    float acc[4][2];
+    float acc[4][4];
     clear(acc);
-    mm<false, true, true, 2>(acc, s.k, s.k, ty, tx);
+    mm<false, true, true, 4>(acc, s.k, s.k, ty, tx);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int t = 4 * ty + i, u = col<2, true>(tx, j);
+        for (int j = 0; j < 4; ++j) {
+            const int t = 4 * ty + i, u = col<4, true>(tx, j);
             s.a[t * kLd + u] = t > u ? acc[i][j] * s.gates.between(t, u) * s.gates.beta[u] : 0.f;
         }
     __syncthreads();
@@ -242,33 +276,33 @@ gated_delta_bwd_local_kernel(Args p) {
     const size_t at = ((size_t)bh * p.NC + n) * kMat;
     store_matrix(p.wT + at, s.t);
     clear(acc);
-    mm<false, true, true, 2>(acc, s.q, s.k, ty, tx);
+    mm<false, true, true, 4>(acc, s.q, s.k, ty, tx);
     __syncthreads();   // A's last use was in invert
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int t = 4 * ty + i, u = col<2, true>(tx, j);
+        for (int j = 0; j < 4; ++j) {
+            const int t = 4 * ty + i, u = col<4, true>(tx, j);
             s.a[t * kLd + u] = t >= u ? p.in.scale * acc[i][j] * s.gates.between(t, u) : 0.f;
         }
     // q <- scale g q
     {
-        const int r = tid >> 3, c = 8 * (tid & 7);
+        const int r = tid >> 2, c = 16 * (tid & 3);
         const float f = p.in.scale * s.gates.g[r];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s.q[r * kLd + c + i] *= f;
+        for (int i = 0; i < 16; ++i) s.q[r * kLd + c + i] *= f;
     }
     __syncthreads();
     clear(acc);
-    mm<true, false, false, 2>(acc, s.a, s.dy, ty, tx);
+    mm<true, false, false, 4>(acc, s.a, s.dy, ty, tx);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        store_cols<2>(p.wX + at + (4 * ty + i) * C + 2 * tx, acc[i]);
+        store_cols<4>(p.wX + at + (4 * ty + i) * C + 4 * tx, acc[i]);
     clear(acc);
-    mm<true, false, false, 2>(acc, s.q, s.dy, ty, tx);
+    mm<true, false, false, 4>(acc, s.q, s.dy, ty, tx);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        store_cols<2>(p.wG + at + (4 * ty + i) * C + 2 * tx, acc[i]);
+        store_cols<4>(p.wG + at + (4 * ty + i) * C + 4 * tx, acc[i]);
 }
 
 // ---- 2: the states forward, the state gradients backward and dV
@@ -417,11 +451,11 @@ gated_delta_bwd_out_kernel(Args p) {
     OutSmem& s = *reinterpret_cast<OutSmem*>(raw);
     const int n = blockIdx.x % p.NC, bk = blockIdx.x / p.NC;
     const int H = p.in.H, HK = p.in.HK, T = p.in.T, b = bk / HK, hk = bk - b * HK, per = H / HK;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ty = tid >> 5, tx = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ty = tid >> 4, tx = tid & 15;
     const int t0 = n * C;
     load_tokens(s.q, (const float*)p.in.q + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, t0, T);
     load_tokens(s.k, (const float*)p.in.k + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, t0, T);
-    float dq[4][2], dk[4][2];
+    float dq[4][4], dk[4][4];
     clear(dq);
     clear(dk);
     for (int h = hk * per; h < (hk + 1) * per; ++h) {
@@ -433,16 +467,16 @@ gated_delta_bwd_out_kernel(Args p) {
         load_matrix(s.g, p.wG + at);
         load_gates(s.gates, (const float*)p.in.omega, (const float*)p.in.beta, (size_t)b * T * H + h, H, t0, T);
         __syncthreads();
-        float acc[4][2], bcc[4][2], w[4][2], cs[2] = {0.f, 0.f};
+        float acc[4][4], bcc[4][4], w[4][4], cs[4] = {0.f, 0.f, 0.f, 0.f};
         clear(acc);
         clear(bcc);
-        mm<false, true, true, 2>(acc, s.q, s.k, ty, tx);
-        mm<false, true, true, 2>(bcc, s.dy, s.e, ty, tx);
+        mm<false, true, true, 4>(acc, s.q, s.k, ty, tx);
+        mm<false, true, true, 4>(bcc, s.dy, s.e, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int t = 4 * ty + i, u = col<2, true>(tx, j);
+            for (int j = 0; j < 4; ++j) {
+                const int t = 4 * ty + i, u = col<4, true>(tx, j);
                 const float d = t >= u ? p.in.scale * s.gates.between(t, u) : 0.f;
                 const float x = t >= u ? bcc[i][j] * d * acc[i][j] : 0.f;   // P_ts dY_t . E_s
                 cs[j] += x;
@@ -451,13 +485,13 @@ gated_delta_bwd_out_kernel(Args p) {
             }
         clear(acc);
         clear(bcc);
-        mm<false, true, true, 2>(acc, s.k, s.k, ty, tx);
-        mm<false, true, true, 2>(bcc, s.df, s.e, ty, tx);
+        mm<false, true, true, 4>(acc, s.k, s.k, ty, tx);
+        mm<false, true, true, 4>(bcc, s.df, s.e, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int t = 4 * ty + i, u = col<2, true>(tx, j);
+            for (int j = 0; j < 4; ++j) {
+                const int t = 4 * ty + i, u = col<4, true>(tx, j);
                 const float d = t > u ? s.gates.between(t, u) : 0.f;
                 const float x = t > u ? bcc[i][j] * d * acc[i][j] : 0.f;    // M_ts dF_t . E_s
                 cs[j] -= x;
@@ -467,7 +501,7 @@ gated_delta_bwd_out_kernel(Args p) {
                 if (t > u) s.dm[u * kLd + t] = m;
             }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) s.cols[ty][col<2, true>(tx, j)] = cs[j];
+        for (int j = 0; j < 4; ++j) s.cols[ty][col<4, true>(tx, j)] = cs[j];
         // <G, S>
         float gs = 0.f;
         for (int i = tid; i < C * C; i += kThreads) {
@@ -477,11 +511,11 @@ gated_delta_bwd_out_kernel(Args p) {
         gs = warp_sum(gs);
         if (lane == 0) s.red[warp] = gs;
         __syncthreads();
-        mm<false, false, true, 2>(dq, s.dp, s.k, ty, tx);
-        mm<true, false, true, 2>(dk, s.dp, s.q, ty, tx);
-        mm<false, false, true, 2>(dk, s.dm, s.k, ty, tx);
+        mm<false, false, true, 4>(dq, s.dp, s.k, ty, tx);
+        mm<true, false, true, 4>(dk, s.dp, s.q, ty, tx);
+        mm<false, false, true, 4>(dk, s.dm, s.k, ty, tx);
         clear(acc);
-        mm<false, true, true, 2>(acc, s.dy, s.s, ty, tx);
+        mm<false, true, true, 4>(acc, s.dy, s.s, ty, tx);
         float rd[4], ke[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -489,43 +523,43 @@ gated_delta_bwd_out_kernel(Args p) {
             const float f = p.in.scale * s.gates.g[t];
             rd[i] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 const float x = f * acc[i][j];
                 dq[i][j] += x;
-                rd[i] = fmaf(s.q[t * kLd + col<2, true>(tx, j)], x, rd[i]);
+                rd[i] = fmaf(s.q[t * kLd + col<4, true>(tx, j)], x, rd[i]);
             }
         }
         clear(acc);
-        mm<false, true, true, 2>(acc, s.df, s.s, ty, tx);
+        mm<false, true, true, 4>(acc, s.df, s.s, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = 4 * ty + i;
             const float f = s.gates.g[t];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 const float x = f * acc[i][j];
                 dk[i][j] -= x;
-                rd[i] = fmaf(-s.k[t * kLd + col<2, true>(tx, j)], x, rd[i]);
+                rd[i] = fmaf(-s.k[t * kLd + col<4, true>(tx, j)], x, rd[i]);
             }
         }
         clear(acc);
-        mm<false, true, true, 2>(acc, s.e, s.g, ty, tx);
+        mm<false, true, true, 4>(acc, s.e, s.g, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = 4 * ty + i;
             const float f = s.gates.to_end[t];
             ke[i] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 const float x = f * acc[i][j];
                 dk[i][j] = fmaf(s.gates.beta[t], x, dk[i][j]);
-                ke[i] = fmaf(s.k[t * kLd + col<2, true>(tx, j)], x, ke[i]);
+                ke[i] = fmaf(s.k[t * kLd + col<4, true>(tx, j)], x, ke[i]);
             }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
+            for (int o = 8; o > 0; o >>= 1) {
                 rd[i] += __shfl_xor_sync(0xffffffffu, rd[i], o);
                 ke[i] += __shfl_xor_sync(0xffffffffu, ke[i], o);
             }
@@ -566,9 +600,9 @@ gated_delta_bwd_out_kernel(Args p) {
         const int t = t0 + 4 * ty + i;
         if (t >= T) continue;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            oq[(size_t)t * HK * C + col<2, true>(tx, j)] = dq[i][j];
-            ok[(size_t)t * HK * C + col<2, true>(tx, j)] = dk[i][j];
+        for (int j = 0; j < 4; ++j) {
+            oq[(size_t)t * HK * C + col<4, true>(tx, j)] = dq[i][j];
+            ok[(size_t)t * HK * C + col<4, true>(tx, j)] = dk[i][j];
         }
     }
 }
