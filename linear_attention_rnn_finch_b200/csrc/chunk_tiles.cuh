@@ -58,6 +58,13 @@ __device__ __forceinline__ void tmem_ld16x4(uint32_t taddr, uint32_t (&v)[16]) {
           "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(taddr));
 }
+// The same shape repeated twice: columns col + 8k + 2(l%4) + {0,1}, k = 0, 1.
+__device__ __forceinline__ void tmem_ld16x2_256(uint32_t taddr, uint32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+                   "=r"(v[7])
+                 : "r"(taddr));
+}
 // The same shape repeated 8 times: columns col + 8k + 2(l%4) + {0,1}, k = 0..7.
 __device__ __forceinline__ void tmem_ld16x8(uint32_t taddr, uint32_t (&v)[32]) {
     asm volatile(

@@ -13,9 +13,8 @@
 // tokens: products with S and G contract value columns, which the chains keep on different warps.
 //
 // S, G, E and dF pass between the launches as two bf16 parts (2^-17 of the value, what the
-// products take anyway) in the order of operand fragments: the chain turns them in registers
-// (movmatrix) and stores 16 bytes a lane, and they are read back with neither swizzle nor
-// ldmatrix.  64 KB a head and block.
+// products take anyway), transposed ([value][key] and [value][token], as the chains hold them)
+// and in the 128-byte-swizzled layout of a tcgen05.mma operand.  64 KB a head and block.
 #include "common.cuh"
 #include "gated_delta.h"
 #include "gated_delta_tiles.cuh"
@@ -36,7 +35,7 @@ struct Args {
     GdrIn in;
     GdrGrads g;
     const float* s_in;
-    uint8_t* ws;     // [head][block][S, E, G, dF]
+    uint8_t* ws;     // [head][block][S, E, G, dF]: hi, then lo part of each
     int blocks;
     // segments of the sequence (gated_delta_segments.cu): A, then the states and the gradients at
     // the borders, each [head][count - 1][64][64] fp32
@@ -44,32 +43,23 @@ struct Args {
     float *a, *s, *d;
 };
 
-__device__ __forceinline__ uint32_t turn(uint32_t x) {
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-
-// A chain warp's state as the B operand [value][key] of 16 value columns: a quad holds both
-// halves of k for two adjacent key tiles.
-__device__ __forceinline__ void put_state(uint8_t* dst, const float (&S)[8][4], int warp, int lane) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t hi[4], lo[4];
-        split_a(hi, lo, S[2 * i], S[2 * i + 1]);
-        uint8_t* at = dst + ((warp * 4 + i) * 32 + lane) * 16;
-        *reinterpret_cast<uint4*>(at) = make_uint4(turn(hi[0]), turn(hi[1]), turn(hi[2]), turn(hi[3]));
-        *reinterpret_cast<uint4*>(at + kPart) = make_uint4(turn(lo[0]), turn(lo[1]), turn(lo[2]), turn(lo[3]));
-    }
-}
-// A sub-chunk's 16 tokens x 16 value columns as an A operand [token][value] (and, its registers
-// taken as 0, 2 and 1, 3, the B operand of the two token tiles).
-__device__ __forceinline__ void put_rows(uint8_t* dst, const float (&e)[2][4], int j, int warp, int lane) {
+// Two adjacent accumulators of chain warp `warp` (16 value columns x 16 keys or tokens, from
+// chunk 2 i of the row on) into a matrix of the workspace, as two parts, through buf (two 16 x 16
+// tiles of the warp's own) so that the stores are whole sectors.
+__device__ __forceinline__ void put(uint8_t* dst, const float (&x)[4], const float (&y)[4], int i, int warp, int lane,
+                                    uint8_t* buf) {
     uint32_t hi[4], lo[4];
-    split_a(hi, lo, e[0], e[1]);
-    uint8_t* at = dst + ((j * 4 + warp) * 32 + lane) * 16;
-    *reinterpret_cast<uint4*>(at) = make_uint4(turn(hi[0]), turn(hi[2]), turn(hi[1]), turn(hi[3]));
-    *reinterpret_cast<uint4*>(at + kPart) = make_uint4(turn(lo[0]), turn(lo[2]), turn(lo[1]), turn(lo[3]));
+    split_a(hi, lo, x, y);
+    const uint32_t at = addr16_bt(ptx::smem_addr(buf), lane);
+    __syncwarp();
+    stsm4(at, hi);
+    stsm4(at + kTile16, lo);
+    __syncwarp();
+    const int row = lane >> 1;
+    const uint8_t* from = buf + off16(row, lane & 1);
+    uint8_t* to = dst + sw_off(16 * warp + row, 2 * i + (lane & 1));
+    *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+    *reinterpret_cast<uint4*>(to + kPart) = *reinterpret_cast<const uint4*>(from + kTile16);
 }
 
 // ------------------------------------------------------------------ the chains
@@ -79,7 +69,7 @@ struct ChainSmem {
     uint8_t q[kStages][kTileBytes];   // backward chain
     Prep prep[2];
     float at[kChainWarps][kSub * 20];
-    uint8_t y[kChainWarps][kTile16];
+    uint8_t y[kChainWarps][2 * kTile16];
 };
 
 // Segment `seg` of head bh from the state (or gradient) `from` (null: zero; `unit`: the identity,
@@ -145,7 +135,10 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh, int s
         const Prep& pr = s.prep[m & 1];
         const uint32_t pt = ptx::smem_addr(pr.t), pp = ptx::smem_addr(pr.p);
         uint8_t* wb = ws + (size_t)block(m) * kBlockBytes;
-        if (kStore) put_state(wb, S, warp, lane);
+        if (kStore) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) put(wb, S[2 * i], S[2 * i + 1], i, warp, lane, s.y[warp]);
+        }
 #pragma unroll 1
         for (int i0 = 0; i0 < kSubs; ++i0) {
             const int j = kBack ? kSubs - 1 - i0 : i0, row = kSub * j;
@@ -182,7 +175,7 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh, int s
 #pragma unroll
                 for (int u = 0; u < 2; ++u) value_minus(f[u], g[u], xv[2 * u], xv[2 * u + 1]);
                 times_t(e, f, pt + j * kTile16, lane);
-                if (kStore) put_rows(wb + kMat, e, j, warp, lane);
+                if (kStore) put(wb + kMat, e[0], e[1], j, warp, lane, s.y[warp]);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) scale_cols(e[u], make_float2(bt[u].x * te[u].x, bt[u].y * te[u].y));
                 update_state(S, pr.g_end[j], e, kt + abt);
@@ -201,7 +194,7 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh, int s
                 times_t<true>(e, f, pt + j * kTile16, lane);
                 if (kStore)
                     store_tokens(dv + (size_t)(t0 + row) * H * C, (size_t)H * C, T - t0 - row, e, s.y[warp], lane);
-                if (kStore) put_rows(wb + kMat, e, j, warp, lane);
+                if (kStore) put(wb + kMat, e[0], e[1], j, warp, lane, s.y[warp]);
                 // G^T = g_16 G^T + (scale g dY)^T Q - (g dF)^T K
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
@@ -263,40 +256,50 @@ gated_delta_bwd_maps_kernel(const __grid_constant__ Args p) {
 }
 
 // ------------------------------------------------------------------ dQ, dK, dbeta, domega
-// Eight warps: warp (w, half) owns tokens 16 w .. 16 w + 15 as rows and 32 key channels of dQ and
-// dK.  Per value head: products over value columns with S and G; then the ten 16 x 16 tiles of
-// the lower triangles dP and dM, dealt out to the warps and put, as two bf16 parts, over S and
-// G's place; then their products with K and Q, rows and columns, the same work for every warp.
-// 128 registers and 97 KB: two CTAs an SM, of which one loads while the other computes.  (Four
-// warps with whole rows of keys took 255 registers and left the schedulers two warps each: B8
-// T1024 H32 216 us against XXX.)
+// A CTA per key head and block; 64 x 64 x 64 products on tcgen05 (M = N = 64, fp32 in TMEM), three
+// groups a value head, each issued by one thread once the last one's results are read:
+//     dY S^T, dF S^T, E G^T and Q K^T;   K K^T, dY E^T and dF E^T;   dP K and dP^T Q + (dM + dM^T) K,
+// dP and dM, as two bf16 parts, over S and G's place.  Warp (w, half) reads tokens
+// 16 w .. 16 w + 15 and 32 columns of each result, in mma accumulator layout.  256 TMEM columns,
+// 94 KB and 128 registers: two CTAs an SM, of which one loads while the other computes.  (The same
+// on mma.sync: operand loads kept the shared-memory pipe 60 % busy, 749 us at B8 T4096 H32.)
 constexpr int kOutThreads = 256;
+constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kKK = ptx::idesc_bf16(64, 64, 0, 0), kKM = ptx::idesc_bf16(64, 64, 0, 1);
+constexpr uint32_t kMM = ptx::idesc_bf16(64, 64, 1, 1);
+constexpr long long kSpin = 2000000000LL;   // cycles a wait may take: about a second
 
 struct OutSmem {
     uint8_t q[kTileBytes], k[kTileBytes], dy[kTileBytes];
     union {
         struct {
-            uint8_t s[kMat], g[kMat];
+            uint8_t s[kMat], g[kMat];                       // [value][key]
         };
         struct {
-            uint8_t dp[2][kTileBytes], dm[2][kTileBytes];   // [t][s], hi and lo parts
+            uint8_t dp[2][kTileBytes], dm[2][kTileBytes];   // [t][s]
         };
     };
-    uint8_t e[kMat], df[kMat];
+    uint8_t e[kMat], df[kMat];                              // [value][token]
     Gates gates;
     float cols[4][C];      // column sums of P dY E - M dF E over each row tile
     float rows[4][C];      // [s tile][t]: row sums of the same, times b_s, left of the diagonal
     float reads[2][C], kte[2][C];
     float gs[8];
     float diag[4][kSub * 17];
+    uint64_t done;
+    uint32_t tmem;
+    int late;              // a wait ran out
 };
 
-__device__ __forceinline__ void get(uint32_t (&r)[4], const uint8_t* p) {
-    const uint4 x = *reinterpret_cast<const uint4*>(p);
-    r[0] = x.x;
-    r[1] = x.y;
-    r[2] = x.z;
-    r[3] = x.w;
+// D (+)= A B over one 64 x 64 x 64 product.  kA, kB: the operand's rows are the contracted index
+// (MN-major: 16 of them are 2048 bytes on), else its own (K-major: 16 k are 32 bytes on).
+template <bool kA, bool kB>
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b, bool add) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        ptx::mma_bf16(d, kA ? ptx::desc_mnmajor(a + 2048 * k) : ptx::desc_kmajor(a + 32 * k),
+                      kB ? ptx::desc_mnmajor(b + 2048 * k) : ptx::desc_kmajor(b + 32 * k),
+                      kA ? (kB ? kMM : ptx::idesc_bf16(64, 64, 1, 0)) : (kB ? kKM : kKK), add || k > 0);
 }
 
 __global__ void __launch_bounds__(kOutThreads, 2)
@@ -310,225 +313,190 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
     const int t0 = n * C, row = kSub * w;
     const size_t ko = ((size_t)b * T * HK + hk) * C;
     const uint32_t sq = ptx::smem_addr(s.q), sk = ptx::smem_addr(s.k), sy = ptx::smem_addr(s.dy);
-    const uint32_t sp = ptx::smem_addr(s.dp), sm = ptx::smem_addr(s.dm);
+    const uint32_t ss = ptx::smem_addr(s.s), sg = ptx::smem_addr(s.g), se = ptx::smem_addr(s.e), sf = ptx::smem_addr(s.df);
+    if (tid == 0) {
+        ptx::mbar_init(&s.done, 1);
+        ptx::fence_mbar_init();
+        s.late = 0;
+    }
+    if (warp == 0) ptx::tmem_alloc(&s.tmem, kTmemCols);
     copy_block<kOutThreads>(sq, (const bf16*)p.in.q + ko, (size_t)HK * C, t0, T, tid);
     copy_block<kOutThreads>(sk, (const bf16*)p.in.k + ko, (size_t)HK * C, t0, T, tid);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tm = s.tmem, tw = tm + ((uint32_t)(32 * w) << 16);   // this warp's lanes
+    uint32_t phase = 0;
+    // all wait for the group last issued; bounded, and once late no more waits and no more products
+    auto arrived = [&] {
+        if (!s.late && !ptx::mbar_wait(&s.done, phase, kSpin)) s.late = 1;
+        phase ^= 1;
+        ptx::tc_fence_after();
+    };
+    // before the next group: TMEM is read, shared memory written
+    auto ready = [&] {
+        ptx::tc_fence_before();
+        ptx::fence_proxy_async_smem();
+        return __syncthreads_or(s.late) == 0;
+    };
     float dq[4][4], dk[4][4];   // key tiles 4 half .. 4 half + 3
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         clear(dq[i]);
         clear(dk[i]);
     }
-    for (int h = hk * per; h < (hk + 1) * per; ++h) {
+    bool good = true;
+    for (int h = hk * per; h < (hk + 1) * per && good; ++h) {
         const size_t bh = (size_t)b * H + h;
         const uint8_t* wb = p.ws + (bh * p.blocks + n) * kBlockBytes;   // S, E, G, dF
         copy_block<kOutThreads>(sy, (const bf16*)p.g.dy + ((size_t)b * T * H + h) * C, (size_t)H * C, t0, T, tid);
 #pragma unroll
         for (int i = 0; i < (int)(kMat / 16 / kOutThreads); ++i) {
             const int o = (i * kOutThreads + tid) * 16;
-            cp_async16(ptx::smem_addr(s.s) + o, wb + o, true);
-            cp_async16(ptx::smem_addr(s.e) + o, wb + kMat + o, true);
-            cp_async16(ptx::smem_addr(s.g) + o, wb + 2 * kMat + o, true);
-            cp_async16(ptx::smem_addr(s.df) + o, wb + 3 * kMat + o, true);
+            cp_async16(ss + o, wb + o, true);
+            cp_async16(se + o, wb + kMat + o, true);
+            cp_async16(sg + o, wb + 2 * kMat + o, true);
+            cp_async16(sf + o, wb + 3 * kMat + o, true);
         }
         cp_async_commit();
         load_gates(s.gates, (const bf16*)p.in.omega, (const bf16*)p.in.beta, (size_t)b * T * H + h, H, t0, T);
         cp_async_wait<0>();
-        __syncthreads();
-
-        // ---- with the states: dK += b to_end (E G^T), then dQ += scale g (dY S^T), dK -= g (dF S^T)
-        const float gt[2] = {s.gates.g[row + r], s.gates.g[row + r + 8]};
+        if (!(good = ready())) break;
+        if (tid == 0) {   // the smallest terms first
+            ptx::tc_fence_after();
+            product<false, true>(tm, sy, ss + kPart, false);
+            product<false, true>(tm, sy, ss, true);
+            product<true, true>(tm + 64, sf + kPart, ss, false);
+            product<true, true>(tm + 64, sf, ss + kPart, true);
+            product<true, true>(tm + 64, sf, ss, true);
+            product<true, true>(tm + 128, se + kPart, sg, false);
+            product<true, true>(tm + 128, se, sg + kPart, true);
+            product<true, true>(tm + 128, se, sg, true);
+            product<false, false>(tm + 192, sq, sk, false);
+            ptx::mma_commit(&s.done);
+        }
+        // <G, S>
         {
-            const float te[2] = {s.gates.to_end[row + r], s.gates.to_end[row + r + 8]};
-            const float bt[2] = {s.gates.beta[row + r], s.gates.beta[row + r + 8]};
-            float x[4][4], ke[2] = {0.f, 0.f}, gs = 0.f;
+            float gs = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) clear(x[i]);
+            for (int i = 0; i < 2; ++i) {
+                const int o = (i * kOutThreads + tid) * 16;
+                const uint4 a = *reinterpret_cast<const uint4*>(s.s + o), al = *reinterpret_cast<const uint4*>(s.s + kPart + o);
+                const uint4 d = *reinterpret_cast<const uint4*>(s.g + o), dl = *reinterpret_cast<const uint4*>(s.g + kPart + o);
+                const uint32_t av[4] = {a.x, a.y, a.z, a.w}, alv[4] = {al.x, al.y, al.z, al.w};
+                const uint32_t dv[4] = {d.x, d.y, d.z, d.w}, dlv[4] = {dl.x, dl.y, dl.z, dl.w};
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {   // 16 value columns
-                uint32_t ah[4], al[4];
-                get(ah, s.e + ((w * 4 + m) * 32 + lane) * 16);
-                get(al, s.e + kPart + ((w * 4 + m) * 32 + lane) * 16);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t gh[4], gl[4];
-                    const int o = ((m * 4 + 2 * half + i) * 32 + lane) * 16;
-                    get(gh, s.g + o);
-                    get(gl, s.g + kPart + o);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) mma(x[2 * i + u], al, gh[2 * u], gh[2 * u + 1]);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) mma(x[2 * i + u], ah, gl[2 * u], gl[2 * u + 1]);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) mma(x[2 * i + u], ah, gh[2 * u], gh[2 * u + 1]);
-                    if (m == w) {   // <G, S>: 16 value columns of this half of the keys
-                        uint32_t sh[4], sl[4];
-                        get(sh, s.s + o);
-                        get(sl, s.s + kPart + o);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 a = tiles::unpack2(sh[e]), d = tiles::unpack2(sl[e]);
-                            const float2 f = tiles::unpack2(gh[e]), g = tiles::unpack2(gl[e]);
-                            gs = fmaf(a.x + d.x, f.x + g.x, gs);
-                            gs = fmaf(a.y + d.y, f.y + g.y, gs);
-                        }
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float2 x = tiles::unpack2(av[e]), xl = tiles::unpack2(alv[e]);
+                    const float2 y = tiles::unpack2(dv[e]), yl = tiles::unpack2(dlv[e]);
+                    gs = fmaf(x.x + xl.x, y.x + yl.x, gs);
+                    gs = fmaf(x.y + xl.y, y.y + yl.y, gs);
                 }
             }
             gs = warp_sum(gs);
             if (lane == 0) s.gs[warp] = gs;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float2 kv = tiles::unpack2(tiles::lds32(s.k, sw_off(row + r + 8 * e, 4 * half + i) + 2 * c));
-                    const float v0 = te[e] * x[i][2 * e], v1 = te[e] * x[i][2 * e + 1];
-                    dk[i][2 * e] = fmaf(bt[e], v0, dk[i][2 * e]);
-                    dk[i][2 * e + 1] = fmaf(bt[e], v1, dk[i][2 * e + 1]);
-                    ke[e] = fmaf(kv.x, v0, fmaf(kv.y, v1, ke[e]));
-                }
+        }
+        arrived();
+        // ---- with the states: dK += b to_end (E G^T) - g (dF S^T), dQ += scale g (dY S^T)
+        {
+            uint32_t x1[16], x2[16], x3[16];
+            tiles::tmem_ld16x4(tw + 32 * half, x1);
+            tiles::tmem_ld16x4(tw + 64 + 32 * half, x2);
+            tiles::tmem_ld16x4(tw + 128 + 32 * half, x3);
+            ptx::tmem_wait_ld();
+            float ke[2] = {0.f, 0.f}, rd[2] = {0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                ke[e] += __shfl_xor_sync(0xffffffffu, ke[e], 1);
-                ke[e] += __shfl_xor_sync(0xffffffffu, ke[e], 2);
-                if ((lane & 3) == 0) s.kte[half][row + r + 8 * e] = ke[e];
-            }
-        }
-        {
-            float x[4][4], y[4][4], rd[2] = {0.f, 0.f};
+                const int t = row + r + 8 * e;
+                const float gt = s.gates.g[t], sgt = p.in.scale * gt, te = s.gates.to_end[t], bt = s.gates.beta[t];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                clear(x[i]);
-                clear(y[i]);
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                uint32_t fh[4], fl[4], ya[4];
-                ldsm4(ya, step(addr_a(sy, row, 0, lane), m));
-                get(fh, s.df + ((w * 4 + m) * 32 + lane) * 16);
-                get(fl, s.df + kPart + ((w * 4 + m) * 32 + lane) * 16);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t sh[4], sl[4];
-                    const int o = ((m * 4 + 2 * half + i) * 32 + lane) * 16;
-                    get(sh, s.s + o);
-                    get(sl, s.s + kPart + o);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        mma(x[2 * i + u], fl, sh[2 * u], sh[2 * u + 1]);
-                        mma(y[2 * i + u], ya, sl[2 * u], sl[2 * u + 1]);
-                    }
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) mma(x[2 * i + u], fh, sl[2 * u], sl[2 * u + 1]);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        mma(y[2 * i + u], ya, sh[2 * u], sh[2 * u + 1]);
-                        mma(x[2 * i + u], fh, sh[2 * u], sh[2 * u + 1]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t o = sw_off(row + r + 8 * e, 4 * half + i) + 2 * c;
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t o = sw_off(t, 4 * half + i) + 2 * c;
                     const float2 qv = tiles::unpack2(tiles::lds32(s.q, o)), kv = tiles::unpack2(tiles::lds32(s.k, o));
-                    const float sg = p.in.scale * gt[e];
-                    const float y0 = sg * y[i][2 * e], y1 = sg * y[i][2 * e + 1];
-                    const float x0 = gt[e] * x[i][2 * e], x1 = gt[e] * x[i][2 * e + 1];
+                    const float y0 = sgt * __uint_as_float(x1[4 * i + 2 * e]), y1 = sgt * __uint_as_float(x1[4 * i + 2 * e + 1]);
+                    const float f0 = gt * __uint_as_float(x2[4 * i + 2 * e]), f1 = gt * __uint_as_float(x2[4 * i + 2 * e + 1]);
+                    const float v0 = te * __uint_as_float(x3[4 * i + 2 * e]), v1 = te * __uint_as_float(x3[4 * i + 2 * e + 1]);
                     dq[i][2 * e] += y0;
                     dq[i][2 * e + 1] += y1;
-                    dk[i][2 * e] -= x0;
-                    dk[i][2 * e + 1] -= x1;
-                    rd[e] += (qv.x * y0 - kv.x * x0) + (qv.y * y1 - kv.y * x1);
+                    dk[i][2 * e] += fmaf(bt, v0, -f0);
+                    dk[i][2 * e + 1] += fmaf(bt, v1, -f1);
+                    ke[e] = fmaf(kv.x, v0, fmaf(kv.y, v1, ke[e]));
+                    rd[e] += (qv.x * y0 - kv.x * f0) + (qv.y * y1 - kv.y * f1);
                 }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
+                ke[e] += __shfl_xor_sync(0xffffffffu, ke[e], 1);
                 rd[e] += __shfl_xor_sync(0xffffffffu, rd[e], 1);
+                ke[e] += __shfl_xor_sync(0xffffffffu, ke[e], 2);
                 rd[e] += __shfl_xor_sync(0xffffffffu, rd[e], 2);
-                if ((lane & 3) == 0) s.reads[half][row + r + 8 * e] = rd[e];
+                if ((lane & 3) == 0) {
+                    s.kte[half][t] = ke[e];
+                    s.reads[half][t] = rd[e];
+                }
             }
         }
-        __syncthreads();   // S and G are read: their place takes dP and dM
-
-        // ---- the triangles: tile (a, v), rows 16 a, columns 16 v; tile number a (a + 1) / 2 + v
-        for (int tile = warp; tile < 10; tile += 8) {
-            const int a = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, v = tile - a * (a + 1) / 2;
-            float qk[2][4], kk[2][4], ye[2][4], fe[2][4];
+        if (!(good = ready())) break;
+        if (tid == 0) {
+            ptx::tc_fence_after();
+            product<false, false>(tm, sk, sk, false);
+            product<false, true>(tm + 64, sy, se + kPart, false);
+            product<false, true>(tm + 64, sy, se, true);
+            product<true, true>(tm + 128, sf + kPart, se, false);
+            product<true, true>(tm + 128, sf, se + kPart, true);
+            product<true, true>(tm + 128, sf, se, true);
+            ptx::mma_commit(&s.done);
+        }
+        arrived();
+        // ---- the triangles: two tiles of 16 x 16 a warp, those above the diagonal zero
+#pragma unroll 1
+        for (int v = 2 * half; v < 2 * half + 2; ++v) {
+            const int ar = row + r;
+            uint32_t ph[4] = {0, 0, 0, 0}, pl[4] = {0, 0, 0, 0}, mh[4] = {0, 0, 0, 0}, ml[4] = {0, 0, 0, 0};
+            if (v <= w) {
+                uint32_t kk[8], ye[8], fe[8], qk[8];
+                tiles::tmem_ld16x2_256(tw + 16 * v, kk);
+                tiles::tmem_ld16x2_256(tw + 64 + 16 * v, ye);
+                tiles::tmem_ld16x2_256(tw + 128 + 16 * v, fe);
+                tiles::tmem_ld16x2_256(tw + 192 + 16 * v, qk);
+                ptx::tmem_wait_ld();
+                const float hh[2] = {s.gates.hi[ar], s.gates.hi[ar + 8]}, ll[2] = {s.gates.lo[ar], s.gates.lo[ar + 8]};
+                float cs[4] = {0.f, 0.f, 0.f, 0.f}, rw[2] = {0.f, 0.f}, dp[2][4], dm[2][4];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                clear(qk[u]);
-                clear(kk[u]);
-                clear(ye[u]);
-                clear(fe[u]);
-            }
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t kb[4], eh[4], el[4], qa[4], ka[4], ya[4], fh[4], fl[4];
-                ldsm4(kb, step(addr_b(sk, kSub * v, 0, lane), i));
-                ldsm4(qa, step(addr_a(sq, kSub * a, 0, lane), i));
-                ldsm4(ka, step(addr_a(sk, kSub * a, 0, lane), i));
-                ldsm4(ya, step(addr_a(sy, kSub * a, 0, lane), i));
-                get(fh, s.df + ((a * 4 + i) * 32 + lane) * 16);
-                get(fl, s.df + kPart + ((a * 4 + i) * 32 + lane) * 16);
-                get(eh, s.e + ((v * 4 + i) * 32 + lane) * 16);
-                get(el, s.e + kPart + ((v * 4 + i) * 32 + lane) * 16);
+                    for (int x = 0; x < 4; ++x) {
+                        const int cl = 8 * u + c + (x & 1), sc = kSub * v + cl, rl = r + 8 * (x >> 1);
+                        const bool on = v < w || rl >= cl, below = v < w || rl > cl;
+                        const float d = on ? tiles::fast_exp2((hh[x >> 1] - s.gates.hi[sc]) + (ll[x >> 1] - s.gates.lo[sc])) : 0.f;
+                        const float bs = s.gates.beta[sc], ds = p.in.scale * d;
+                        const float y = on ? __uint_as_float(ye[4 * u + x]) : 0.f, f = below ? __uint_as_float(fe[4 * u + x]) : 0.f;
+                        const float sum = ds * __uint_as_float(qk[4 * u + x]) * y - d * __uint_as_float(kk[4 * u + x]) * f;
+                        cs[2 * u + (x & 1)] += sum;
+                        const float wt = below ? bs * sum : 0.f;
+                        rw[x >> 1] += wt;
+                        if (v == w) s.diag[w][rl * 17 + cl] = wt;
+                        dp[u][x] = ds * bs * y;
+                        dm[u][x] = -d * bs * f;
+                    }
+                // column sums over the tile's rows, row sums over its columns
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {   // E's rows as B: registers 0, 2 and 1, 3
-                    mma(qk[u], qa, kb[2 * u], kb[2 * u + 1]);
-                    mma(kk[u], ka, kb[2 * u], kb[2 * u + 1]);
-                    mma(ye[u], ya, el[u], el[u + 2]);
-                    mma(fe[u], fl, eh[u], eh[u + 2]);
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) cs[x] += __shfl_xor_sync(0xffffffffu, cs[x], o);
+                if (lane < 4) {
+                    float* at = &s.cols[w][kSub * v + c];
+                    at[0] = cs[0];
+                    at[1] = cs[1];
+                    at[8] = cs[2];
+                    at[9] = cs[3];
                 }
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    mma(ye[u], ya, eh[u], eh[u + 2]);
-                    mma(fe[u], fh, el[u], el[u + 2]);
+                for (int e = 0; e < 2; ++e) {
+                    rw[e] += __shfl_xor_sync(0xffffffffu, rw[e], 1);
+                    rw[e] += __shfl_xor_sync(0xffffffffu, rw[e], 2);
+                    if ((lane & 3) == 0) s.rows[v][ar + 8 * e] = rw[e];   // read where v < w
                 }
-#pragma unroll
-                for (int u = 0; u < 2; ++u) mma(fe[u], fh, eh[u], eh[u + 2]);
+                split_a(ph, pl, dp[0], dp[1]);
+                split_a(mh, ml, dm[0], dm[1]);
             }
-            const int ar = kSub * a + r;
-            const float hh[2] = {s.gates.hi[ar], s.gates.hi[ar + 8]}, ll[2] = {s.gates.lo[ar], s.gates.lo[ar + 8]};
-            float cs[4] = {0.f, 0.f, 0.f, 0.f}, rw[2] = {0.f, 0.f};
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int cl = 8 * u + c + (x & 1), sc = kSub * v + cl, rl = r + 8 * (x >> 1);
-                    const bool on = v < a || rl >= cl, below = v < a || rl > cl;
-                    const float d = on ? tiles::fast_exp2((hh[x >> 1] - s.gates.hi[sc]) + (ll[x >> 1] - s.gates.lo[sc])) : 0.f;
-                    const float bs = s.gates.beta[sc], ds = p.in.scale * d;
-                    const float y = on ? ye[u][x] : 0.f, f = below ? fe[u][x] : 0.f;
-                    const float sum = ds * qk[u][x] * y - d * kk[u][x] * f;
-                    cs[2 * u + (x & 1)] += sum;
-                    const float wt = below ? bs * sum : 0.f;
-                    rw[x >> 1] += wt;
-                    if (v == a) s.diag[a][rl * 17 + cl] = wt;
-                    ye[u][x] = ds * bs * y;      // dP
-                    fe[u][x] = -d * bs * f;      // dM
-                }
-            // column sums over the tile's rows, row sums over its columns
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) cs[x] += __shfl_xor_sync(0xffffffffu, cs[x], o);
-            if (lane < 4) {
-                float* at = &s.cols[a][kSub * v + c];
-                at[0] = cs[0];
-                at[1] = cs[1];
-                at[8] = cs[2];
-                at[9] = cs[3];
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                rw[e] += __shfl_xor_sync(0xffffffffu, rw[e], 1);
-                rw[e] += __shfl_xor_sync(0xffffffffu, rw[e], 2);
-                if ((lane & 3) == 0) s.rows[v][ar + 8 * e] = rw[e];   // read where v < a
-            }
-            uint32_t ph[4], pl[4], mh[4], ml[4];
-            split_a(ph, pl, ye[0], ye[1]);
-            split_a(mh, ml, fe[0], fe[1]);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const uint32_t o = sw_off(ar + 8 * (x & 1), 2 * v + (x >> 1)) + 2 * c;
@@ -538,54 +506,19 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
                 tiles::sts32(s.dm[1], o, ml[x]);
             }
         }
-        __syncthreads();
-        // ---- rows: dQ += dP K, dK += dM K
-        for (int v = 0; v <= w; ++v) {
-            uint32_t ph[4], pl[4], mh[4], ml[4];
-            const uint32_t at = addr_a(0, row, 2 * v, lane);
-            ldsm4(ph, sp + at);
-            ldsm4(pl, sp + kTileBytes + at);
-            ldsm4(mh, sm + at);
-            ldsm4(ml, sm + kTileBytes + at);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t kb[4];
-                ldsm4t(kb, step(addr_bt(sk, kSub * v, 0, lane), 2 * half + i));
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    mma(dq[2 * i + u], pl, kb[2 * u], kb[2 * u + 1]);
-                    mma(dk[2 * i + u], ml, kb[2 * u], kb[2 * u + 1]);
-                }
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    mma(dq[2 * i + u], ph, kb[2 * u], kb[2 * u + 1]);
-                    mma(dk[2 * i + u], mh, kb[2 * u], kb[2 * u + 1]);
-                }
-            }
-        }
-        // ---- columns: dK += dP^T Q + dM^T K
-        for (int v = w; v < 4; ++v) {
-            uint32_t ph[4], pl[4], mh[4], ml[4];
-            // A operand [s][t] from [t][s] rows: 16 rows from 16 v, columns from 16 w
-            const uint32_t at = sw_off(kSub * v + ((lane >> 4) << 3) + (lane & 7), 2 * w + ((lane >> 3) & 1));
-            ldsm4t(ph, sp + at);
-            ldsm4t(pl, sp + kTileBytes + at);
-            ldsm4t(mh, sm + at);
-            ldsm4t(ml, sm + kTileBytes + at);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t qb[4], kb[4];
-                ldsm4t(qb, step(addr_bt(sq, kSub * v, 0, lane), 2 * half + i));
-                ldsm4t(kb, step(addr_bt(sk, kSub * v, 0, lane), 2 * half + i));
-#pragma unroll
-                for (int u = 0; u < 2; ++u) mma(dk[2 * i + u], pl, qb[2 * u], qb[2 * u + 1]);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) mma(dk[2 * i + u], ml, kb[2 * u], kb[2 * u + 1]);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) mma(dk[2 * i + u], ph, qb[2 * u], qb[2 * u + 1]);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) mma(dk[2 * i + u], mh, kb[2 * u], kb[2 * u + 1]);
-            }
+        if (!(good = ready())) break;
+        if (tid == 0) {
+            const uint32_t sp = ptx::smem_addr(s.dp), sm = ptx::smem_addr(s.dm);
+            ptx::tc_fence_after();
+            product<false, true>(tm, sp + kTileBytes, sk, false);
+            product<false, true>(tm, sp, sk, true);
+            product<true, true>(tm + 64, sp + kTileBytes, sq, false);
+            product<false, true>(tm + 64, sm + kTileBytes, sk, true);
+            product<true, true>(tm + 64, sm + kTileBytes, sk, true);
+            product<true, true>(tm + 64, sp, sq, true);
+            product<false, true>(tm + 64, sm, sk, true);
+            product<true, true>(tm + 64, sm, sk, true);
+            ptx::mma_commit(&s.done);
         }
         // ---- dbeta and domega of the row tile's 16 tokens, a lane a token (lanes 16-31 repeat them)
         if (half == 0) {
@@ -638,18 +571,51 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
                 ((bf16*)p.g.dbeta)[o] = __float2bfloat16_rn(db);
             }
         }
-        __syncthreads();
-    }
-    bf16* oq = (bf16*)p.g.dq + ko + 32 * half;
-    bf16* ok = (bf16*)p.g.dk + ko + 32 * half;
+        arrived();
+        {
+            uint32_t x1[16], x2[16];
+            tiles::tmem_ld16x4(tw + 32 * half, x1);
+            tiles::tmem_ld16x4(tw + 64 + 32 * half, x2);
+            ptx::tmem_wait_ld();
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int t = t0 + row + r + 8 * x;
-        if (t >= T) continue;
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    dq[i][e] += __uint_as_float(x1[4 * i + e]);
+                    dk[i][e] += __uint_as_float(x2[4 * i + e]);
+                }
+        }
+        good = ready();   // also: this head's tiles may be overwritten
+    }
+    // late: the products last issued may be running still; a second chance to end, and NaN results
+    if (!good) {
+        (void)ptx::mbar_wait(&s.done, phase ^ 1, kSpin);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dq[i][e] = dk[i][e] = __int_as_float(0x7fffffff);
+    }
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 0) ptx::tmem_dealloc(tm, kTmemCols);
+    // out through Q's and K's places: whole rows of 128 bytes
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            *reinterpret_cast<uint32_t*>(oq + (size_t)t * HK * C + 8 * i + c) = pack2(dq[i][2 * x], dq[i][2 * x + 1]);
-            *reinterpret_cast<uint32_t*>(ok + (size_t)t * HK * C + 8 * i + c) = pack2(dk[i][2 * x], dk[i][2 * x + 1]);
+            const uint32_t o = sw_off(row + r + 8 * x, 4 * half + i) + 2 * c;
+            tiles::sts32(s.q, o, pack2(dq[i][2 * x], dq[i][2 * x + 1]));
+            tiles::sts32(s.k, o, pack2(dk[i][2 * x], dk[i][2 * x + 1]));
+        }
+    __syncthreads();
+    bf16 *oq = (bf16*)p.g.dq + ko, *ok = (bf16*)p.g.dk + ko;
+#pragma unroll
+    for (int i = 0; i < C * 8 / kOutThreads; ++i) {
+        const int t = (tid >> 3) + i * (kOutThreads / 8), ch = tid & 7;
+        if (t0 + t < T) {
+            const size_t o = (size_t)(t0 + t) * HK * C + 8 * ch;
+            *reinterpret_cast<uint4*>(oq + o) = *reinterpret_cast<const uint4*>(s.q + sw_off(t, ch));
+            *reinterpret_cast<uint4*>(ok + o) = *reinterpret_cast<const uint4*>(s.k + sw_off(t, ch));
         }
     }
 }

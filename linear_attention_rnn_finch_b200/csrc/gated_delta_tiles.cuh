@@ -44,8 +44,12 @@ constexpr int kChainWarps = 4;
 constexpr int kPrepThreads = 128;
 constexpr int kTcThreads = 256;             // chain warps, then as many of preparation
 constexpr uint32_t kTileBytes = C * C * 2;  // 64 rows of 128 bytes
-constexpr int kRow16 = 48;                  // row bytes of a 16 x 16 bf16 tile: no bank conflicts
-constexpr int kTile16 = kSub * kRow16;
+constexpr int kTile16 = kSub * 32;          // a 16 x 16 bf16 tile
+// Its row of 32 bytes, two 16-byte chunks that trade places every four rows: eight rows then lie
+// in different banks.
+__device__ __forceinline__ uint32_t off16(int row, int chunk) {
+    return (uint32_t)(row * 32 + ((chunk ^ ((row >> 2) & 1)) << 4));
+}
 
 // What the preparation hands to the chain for one block.
 struct Prep {
@@ -57,14 +61,12 @@ struct Prep {
     float g_end[kSubs];
 };
 
-// 16 x 16 tile (rows of kRow16 bytes): both n halves of a B operand from [n][k] rows ...
+// ldmatrix address of a 16 x 16 tile: both n halves of a B operand from [n][k] rows ...
 __device__ __forceinline__ uint32_t addr16_b(uint32_t tile, int lane) {
-    return tile + (uint32_t)((((lane >> 4) << 3) + (lane & 7)) * kRow16 + ((lane >> 3) & 1) * 16);
+    return tile + off16(((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1);
 }
 // ... and from [k][n] rows (.trans)
-__device__ __forceinline__ uint32_t addr16_bt(uint32_t tile, int lane) {
-    return tile + (uint32_t)((lane & 15) * kRow16 + (lane >> 4) * 16);
-}
+__device__ __forceinline__ uint32_t addr16_bt(uint32_t tile, int lane) { return tile + off16(lane & 15, lane >> 4); }
 
 // Rows t0 .. t0 + 63 of a token tensor (row stride `step` values) into a tile by `threads`
 // threads; rows at T or beyond as zeros.
@@ -171,15 +173,16 @@ __device__ __forceinline__ void prepare_sub(Prep& out, float* at, uint32_t kt, u
             x[i + 3] = fmaf(-m.w, x[s], x[i + 3]);
         }
     // lanes 0-15 store the first part of their column and the third, lanes 16-31 the second
-    uint8_t* dst = out.t[lane >> 4][j] + 2 * (lane & 15);
+    uint8_t* dst = out.t[lane >> 4][j];
+    const int ch = (lane >> 3) & 1, by = 2 * (lane & 7);
 #pragma unroll
     for (int i = 0; i < kSub; ++i) {
         const __nv_bfloat16 h = __float2bfloat16_rn(x[i]);
         const float rest = x[i] - __bfloat162float(h);
         const __nv_bfloat16 m = __float2bfloat16_rn(rest);
-        *reinterpret_cast<__nv_bfloat16*>(dst + i * kRow16) = lane < 16 ? h : m;
+        *reinterpret_cast<__nv_bfloat16*>(dst + off16(i, ch) + by) = lane < 16 ? h : m;
         if (lane < 16)
-            *reinterpret_cast<__nv_bfloat16*>(out.t[2][j] + 2 * lane + i * kRow16) =
+            *reinterpret_cast<__nv_bfloat16*>(out.t[2][j] + off16(i, ch) + by) =
                 __float2bfloat16_rn(rest - __bfloat162float(m));
     }
     if (kP) {
@@ -189,7 +192,7 @@ __device__ __forceinline__ void prepare_sub(Prep& out, float* at, uint32_t kt, u
             for (int h = 0; h < 2; ++h) {
                 uint32_t a, b;
                 split2(make_float2(qk[n][2 * h], qk[n][2 * h + 1]), a, b);
-                const int o = (r + 8 * h) * kRow16 + (8 * n + c) * 2;
+                const uint32_t o = off16(r + 8 * h, n) + 2 * c;
                 *reinterpret_cast<uint32_t*>(out.p[0][j] + o) = a;
                 *reinterpret_cast<uint32_t*>(out.p[1][j] + o) = b;
             }
@@ -282,13 +285,13 @@ __device__ __forceinline__ void update_state(float (&S)[8][4], float factor, con
 __device__ __forceinline__ void store_tokens(__nv_bfloat16* out, size_t step, int count, const float (&y)[2][4],
                                              uint8_t* tile, int lane) {
     __syncwarp();
-    stsm4t(ptx::smem_addr(tile) + (uint32_t)((((lane >> 4) << 3) + (lane & 7)) * kRow16 + ((lane >> 3) & 1) * 16),
+    stsm4t(ptx::smem_addr(tile) + off16(((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1),
            pack2(y[0][0], y[0][1]), pack2(y[0][2], y[0][3]), pack2(y[1][0], y[1][1]), pack2(y[1][2], y[1][3]));
     __syncwarp();
     const int t = lane >> 1;
     if (t < count)
         *reinterpret_cast<uint4*>(out + (size_t)t * step + 8 * (lane & 1)) =
-            *reinterpret_cast<const uint4*>(tile + t * kRow16 + (lane & 1) * 16);
+            *reinterpret_cast<const uint4*>(tile + off16(t, lane & 1));
 }
 
 }  // namespace gdr
