@@ -265,8 +265,6 @@ gated_delta_bwd_maps_kernel(const __grid_constant__ Args p) {
 // on mma.sync: operand loads kept the shared-memory pipe 60 % busy, 749 us at B8 T4096 H32.)
 constexpr int kOutThreads = 256;
 constexpr uint32_t kTmemCols = 256;
-constexpr uint32_t kKK = ptx::idesc_bf16(64, 64, 0, 0), kKM = ptx::idesc_bf16(64, 64, 0, 1);
-constexpr uint32_t kMM = ptx::idesc_bf16(64, 64, 1, 1);
 constexpr long long kSpin = 2000000000LL;   // cycles a wait may take: about a second
 
 struct OutSmem {
@@ -285,7 +283,7 @@ struct OutSmem {
     float rows[4][C];      // [s tile][t]: row sums of the same, times b_s, left of the diagonal
     float reads[2][C], kte[2][C];
     float gs[8];
-    float diag[4][kSub * 17];
+    float diag[C];         // the same over a token's own tile: rows from it on, columns before it
     uint64_t done;
     uint32_t tmem;
     int late;              // a wait ran out
@@ -295,12 +293,25 @@ struct OutSmem {
 // (MN-major: 16 of them are 2048 bytes on), else its own (K-major: 16 k are 32 bytes on).
 template <bool kA, bool kB>
 __device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b, bool add) {
+    const uint64_t da = kA ? ptx::desc_mnmajor(a) : ptx::desc_kmajor(a), db = kB ? ptx::desc_mnmajor(b) : ptx::desc_kmajor(b);
+    constexpr uint32_t kDesc = ptx::idesc_bf16(64, 64, kA, kB);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        ptx::mma_bf16(d, kA ? ptx::desc_mnmajor(a + 2048 * k) : ptx::desc_kmajor(a + 32 * k),
-                      kB ? ptx::desc_mnmajor(b + 2048 * k) : ptx::desc_kmajor(b + 32 * k),
-                      kA ? (kB ? kMM : ptx::idesc_bf16(64, 64, 1, 0)) : (kB ? kKM : kKK), add || k > 0);
+    for (int k = 0; k < 4; ++k)   // addresses count in 16 bytes
+        ptx::mma_bf16(d, da + (kA ? 128 : 2) * k, db + (kB ? 128 : 2) * k, kDesc, add || k > 0);
 }
+
+// Sums over the eight lanes that share columns c, c + 1, 8 + c, 9 + c (x[0..3]): each step a lane
+// hands half of its columns over and keeps the other.  Lane l < 16 returns column column_of(l)'s.
+__device__ __forceinline__ float column_sums(const float (&x)[4], int lane) {
+    const bool a = lane & 4, b = lane & 8;
+    float k0 = a ? x[2] : x[0], k1 = a ? x[3] : x[1];
+    k0 += __shfl_xor_sync(0xffffffffu, a ? x[0] : x[2], 4);
+    k1 += __shfl_xor_sync(0xffffffffu, a ? x[1] : x[3], 4);
+    float k = b ? k1 : k0;
+    k += __shfl_xor_sync(0xffffffffu, b ? k0 : k1, 8);
+    return k + __shfl_xor_sync(0xffffffffu, k, 16);
+}
+__device__ __forceinline__ int column_of(int lane) { return 2 * (lane & 3) + 8 * ((lane >> 2) & 1) + ((lane >> 3) & 1); }
 
 __global__ void __launch_bounds__(kOutThreads, 2)
 gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
@@ -326,6 +337,9 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tm = s.tmem, tw = tm + ((uint32_t)(32 * w) << 16);   // this warp's lanes
+    // one thread issues; the warp's number through a shuffle, so that the branch and with it the
+    // descriptors stay in uniform registers
+    const bool issuer = __shfl_sync(0xffffffffu, warp, 0) == 0;
     uint32_t phase = 0;
     // all wait for the group last issued; bounded, and once late no more waits and no more products
     auto arrived = [&] {
@@ -349,6 +363,7 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
     for (int h = hk * per; h < (hk + 1) * per && good; ++h) {
         const size_t bh = (size_t)b * H + h;
         const uint8_t* wb = p.ws + (bh * p.blocks + n) * kBlockBytes;   // S, E, G, dF
+        const auto raw_gates = fetch_gates((const bf16*)p.in.omega, (const bf16*)p.in.beta, (size_t)b * T * H + h, H, t0, T);
         copy_block<kOutThreads>(sy, (const bf16*)p.g.dy + ((size_t)b * T * H + h) * C, (size_t)H * C, t0, T, tid);
 #pragma unroll
         for (int i = 0; i < (int)(kMat / 16 / kOutThreads); ++i) {
@@ -359,10 +374,10 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
             cp_async16(sf + o, wb + 3 * kMat + o, true);
         }
         cp_async_commit();
-        load_gates(s.gates, (const bf16*)p.in.omega, (const bf16*)p.in.beta, (size_t)b * T * H + h, H, t0, T);
+        put_gates(s.gates, raw_gates, t0, T);
         cp_async_wait<0>();
         if (!(good = ready())) break;
-        if (tid == 0) {   // the smallest terms first
+        if (issuer && ptx::elect_one()) {   // the smallest terms first
             ptx::tc_fence_after();
             product<false, true>(tm, sy, ss + kPart, false);
             product<false, true>(tm, sy, ss, true);
@@ -372,8 +387,8 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
             product<true, true>(tm + 128, se + kPart, sg, false);
             product<true, true>(tm + 128, se, sg + kPart, true);
             product<true, true>(tm + 128, se, sg, true);
-            product<false, false>(tm + 192, sq, sk, false);
             ptx::mma_commit(&s.done);
+            product<false, false>(tm + 192, sq, sk, false);   // awaited with the next group
         }
         // <G, S>
         {
@@ -434,7 +449,7 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
             }
         }
         if (!(good = ready())) break;
-        if (tid == 0) {
+        if (issuer && ptx::elect_one()) {
             ptx::tc_fence_after();
             product<false, false>(tm, sk, sk, false);
             product<false, true>(tm + 64, sy, se + kPart, false);
@@ -458,36 +473,59 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
                 tiles::tmem_ld16x2_256(tw + 192 + 16 * v, qk);
                 ptx::tmem_wait_ld();
                 const float hh[2] = {s.gates.hi[ar], s.gates.hi[ar + 8]}, ll[2] = {s.gates.lo[ar], s.gates.lo[ar + 8]};
-                float cs[4] = {0.f, 0.f, 0.f, 0.f}, rw[2] = {0.f, 0.f}, dp[2][4], dm[2][4];
+                float cs[4], rw[2] = {0.f, 0.f}, dp[2][4], dm[2][4], wt[2][4];
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         const int cl = 8 * u + c + (x & 1), sc = kSub * v + cl, rl = r + 8 * (x >> 1);
-                        const bool on = v < w || rl >= cl, below = v < w || rl > cl;
-                        const float d = on ? tiles::fast_exp2((hh[x >> 1] - s.gates.hi[sc]) + (ll[x >> 1] - s.gates.lo[sc])) : 0.f;
-                        const float bs = s.gates.beta[sc], ds = p.in.scale * d;
-                        const float y = on ? __uint_as_float(ye[4 * u + x]) : 0.f, f = below ? __uint_as_float(fe[4 * u + x]) : 0.f;
-                        const float sum = ds * __uint_as_float(qk[4 * u + x]) * y - d * __uint_as_float(kk[4 * u + x]) * f;
-                        cs[2 * u + (x & 1)] += sum;
-                        const float wt = below ? bs * sum : 0.f;
-                        rw[x >> 1] += wt;
-                        if (v == w) s.diag[w][rl * 17 + cl] = wt;
-                        dp[u][x] = ds * bs * y;
-                        dm[u][x] = -d * bs * f;
+                        const bool on = v < w || rl >= cl;
+                        float d = tiles::fast_exp2((hh[x >> 1] - s.gates.hi[sc]) + (ll[x >> 1] - s.gates.lo[sc]));
+                        d = on ? d : 0.f;   // above the diagonal it may be infinite
+                        const float bs = s.gates.beta[sc], db = d * bs;
+                        const float y = on ? p.in.scale * __uint_as_float(ye[4 * u + x]) : 0.f;
+                        const float f = v < w || rl > cl ? __uint_as_float(fe[4 * u + x]) : 0.f;
+                        const float sum = d * (__uint_as_float(qk[4 * u + x]) * y - __uint_as_float(kk[4 * u + x]) * f);
+                        if (x < 2) cs[2 * u + x] = sum;
+                        else cs[2 * u + x - 2] += sum;
+                        wt[u][x] = v < w || rl > cl ? bs * sum : 0.f;
+                        rw[x >> 1] += wt[u][x];
+                        dp[u][x] = db * y;
+                        dm[u][x] = -db * f;
                     }
-                // column sums over the tile's rows, row sums over its columns
+                if (v == w) {
+                    // inside the diagonal tile: for each column u the sum over rows from u on of
+                    // the row's entries before u
+                    float before[2][4];
+                    const int q = lane & 3;
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
+                    for (int e = 0; e < 2; ++e) {
+                        float left = 0.f;   // the row's first eight columns
 #pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) cs[x] += __shfl_xor_sync(0xffffffffu, cs[x], o);
-                if (lane < 4) {
-                    float* at = &s.cols[w][kSub * v + c];
-                    at[0] = cs[0];
-                    at[1] = cs[1];
-                    at[8] = cs[2];
-                    at[9] = cs[3];
+                        for (int u = 0; u < 2; ++u) {
+                            const float pair = wt[u][2 * e] + wt[u][2 * e + 1];
+                            float x = __shfl_up_sync(0xffffffffu, pair, 1, 4);
+                            float run = q > 0 ? x : 0.f;
+                            x = __shfl_up_sync(0xffffffffu, run + pair, 2, 4);
+                            // run: the pair before; x: the two before that one
+                            run += q > 1 ? x : 0.f;
+                            before[u][2 * e] = left + run;
+                            before[u][2 * e + 1] = left + run + wt[u][2 * e];
+                            left = __shfl_sync(0xffffffffu, run + pair, 3, 4);
+                        }
+                    }
+                    float ds[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int u = x >> 1, cl = 8 * u + c + (x & 1);
+                        ds[x] = (r >= cl ? before[u][x & 1] : 0.f) + (r + 8 >= cl ? before[u][2 + (x & 1)] : 0.f);
+                    }
+                    const float dsum = column_sums(ds, lane);
+                    if (lane < 16) s.diag[row + column_of(lane)] = dsum;
                 }
+                // column sums over the tile's rows, row sums over its columns
+                const float col = column_sums(cs, lane);
+                if (lane < 16) s.cols[w][kSub * v + column_of(lane)] = col;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     rw[e] += __shfl_xor_sync(0xffffffffu, rw[e], 1);
@@ -507,7 +545,7 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
             }
         }
         if (!(good = ready())) break;
-        if (tid == 0) {
+        if (issuer && ptx::elect_one()) {
             const uint32_t sp = ptx::smem_addr(s.dp), sm = ptx::smem_addr(s.dm);
             ptx::tc_fence_after();
             product<false, true>(tm, sp + kTileBytes, sk, false);
@@ -521,15 +559,8 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
             ptx::mma_commit(&s.done);
         }
         // ---- dbeta and domega of the row tile's 16 tokens, a lane a token (lanes 16-31 repeat them)
-        if (half == 0) {
+        if (half == 1) {   // not the issuing warp
             const int l = lane & 15, t = row + l;
-            // inside the diagonal tile: sums over t' >= t, s < t, by column sums from below
-            float dg = 0.f;
-            if (lane < 16)
-                for (int i = kSub - 1; i > l; --i) s.diag[w][i * 17 + l] = dg += s.diag[w][i * 17 + l];
-            __syncwarp();
-            dg = 0.f;
-            for (int i = 0; i < l; ++i) dg += s.diag[w][l * 17 + i];
             // rows of this tile from t on, columns of the tiles to the left
             float rs = s.reads[0][t] + s.reads[1][t];
             for (int v = 0; v < w; ++v) rs += s.rows[v][t];
@@ -564,7 +595,7 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
             float gsum = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) gsum += s.gs[i];
-            const float dl = ((dg + rs) + later) + (before + pre) + s.gates.g[C - 1] * gsum;
+            const float dl = ((s.diag[t] + rs) + later) + (before + pre) + s.gates.g[C - 1] * gsum;
             if (lane < 16 && t0 + t < T) {
                 const size_t o = ((size_t)b * T + t0 + t) * H + h;
                 ((bf16*)p.g.domega)[o] = __float2bfloat16_rn(-s.gates.rate[t] * dl);

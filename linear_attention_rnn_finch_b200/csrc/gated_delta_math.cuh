@@ -49,10 +49,28 @@ struct Gates {
 };
 
 // Tokens at T or beyond neither decay nor write (log w = 0, beta = 0).  Warp 0 does it, two
-// tokens a lane; the caller's barrier publishes it.
+// tokens a lane: the loads (fetch) ahead of the rest; the caller's barrier publishes it.
 template <typename IO>
-__device__ __forceinline__ void load_gates(Gates& s, const IO* omega, const IO* beta, size_t base,
-                                           int stride, int t0, int T) {
+struct RawGates {
+    IO omega[2], beta[2];
+};
+template <typename IO>
+__device__ __forceinline__ RawGates<IO> fetch_gates(const IO* omega, const IO* beta, size_t base, int stride,
+                                                    int t0, int T) {
+    RawGates<IO> r{};
+    if (threadIdx.x < 32)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * threadIdx.x + i;
+            if (t0 + t < T) {
+                r.omega[i] = omega[base + (size_t)(t0 + t) * stride];
+                r.beta[i] = beta[base + (size_t)(t0 + t) * stride];
+            }
+        }
+    return r;
+}
+template <typename IO>
+__device__ __forceinline__ void put_gates(Gates& s, const RawGates<IO>& raw, int t0, int T) {
     if (threadIdx.x >= 32) return;
     const int lane = threadIdx.x;
     double l[2], run = 0.0;
@@ -60,10 +78,9 @@ __device__ __forceinline__ void load_gates(Gates& s, const IO* omega, const IO* 
     for (int i = 0; i < 2; ++i) {
         const int t = 2 * lane + i;
         const bool in = t0 + t < T;
-        const size_t o = base + (size_t)(t0 + t) * stride;
-        const float r = in ? decay_rate(to_f32(omega[o])) : 0.f;
+        const float r = in ? decay_rate(to_f32(raw.omega[i])) : 0.f;
         s.rate[t] = r;
-        s.beta[t] = in ? to_f32(beta[o]) : 0.f;
+        s.beta[t] = in ? to_f32(raw.beta[i]) : 0.f;
         run += -1.4426950408889634 * (double)r;
         l[i] = run;
     }
@@ -85,6 +102,11 @@ __device__ __forceinline__ void load_gates(Gates& s, const IO* omega, const IO* 
         s.g[t] = exp2f((float)x);
         s.to_end[t] = exp2f((float)(total - x));
     }
+}
+template <typename IO>
+__device__ __forceinline__ void load_gates(Gates& s, const IO* omega, const IO* beta, size_t base,
+                                           int stride, int t0, int T) {
+    put_gates(s, fetch_gates(omega, beta, base, stride, t0, T), t0, T);
 }
 
 }  // namespace gdr
