@@ -139,7 +139,7 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh, int s
 #pragma unroll
             for (int i = 0; i < 4; ++i) put(wb, S[2 * i], S[2 * i + 1], i, warp, lane, s.y[warp]);
         }
-#pragma unroll 1
+#pragma unroll 2
         for (int i0 = 0; i0 < kSubs; ++i0) {
             const int j = kBack ? kSubs - 1 - i0 : i0, row = kSub * j;
             const uint32_t kt = sk + o + row * 128;

@@ -101,7 +101,7 @@ __device__ __forceinline__ void walk(const Args& p, int bh, int seg, bool unit, 
         const Prep& pr = s.prep[n & 1];
         const uint32_t pt = ptx::smem_addr(pr.t), pp = ptx::smem_addr(pr.p);
         const int subs = min(kSubs, (T - n * C + kSub - 1) / kSub);
-#pragma unroll 1
+#pragma unroll 2
         for (int j = 0; j < subs; ++j) {
             const int row = kSub * j;
             const uint32_t kt = sk + o + row * 128;

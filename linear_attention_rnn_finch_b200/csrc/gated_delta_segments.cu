@@ -64,13 +64,13 @@ gated_delta_join_kernel(const float* __restrict__ a, float* m, int last) {
 
 // By what the launches then take: a CTA needs `full` us for a block with outputs and `part`
 // without, and a second CTA on an SM as long again (the schedulers are full); a border costs 1.2
-// us, the launches more 6 us.
+// us, the launches more 6 us; a gain below a twentieth is not taken.
 GdrSegments gdr_segments(int B, int T, int H, int ctas, int maps, float full, float part) {
     const int blocks = (T + C - 1) / C;
     const long heads = (long)B * H;
     auto turns = [](long n) { return (double)((n + kSms - 1) / kSms); };
     GdrSegments best{1, blocks};
-    double least = turns(heads * ctas) * blocks * full;
+    double least = 0.95 * turns(heads * ctas) * blocks * full;
     for (int want = 2; want <= 64 && heads * want <= 4 * kSms && 4 * want <= blocks; ++want) {
         const int each = (blocks + want - 1) / want, n = (blocks + each - 1) / each;
         if (n < 2) continue;
