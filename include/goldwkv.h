@@ -372,6 +372,8 @@ wkv_status gold_decompress(const void *x0, const void *c, const void *w_ku, cons
  *                               with beta = 0 writes nothing, and with omega = -inf as well it
  *                               leaves the state as it is (padding; its other inputs finite)
  *   state       [B][H][D][D] fp32
+ * Tokens are worked on in groups: a NaN or an infinity in one reaches its head's outputs from it
+ * on, as the recurrence has it, and may reach those of the 63 tokens before it.
  * Keys are taken as given: the rule is stable for |k_t| <= 1 and beta in [0, 2], which is the
  * caller's to see to (unit-length keys).  scale must be finite.  The conventions at the top of
  * this file hold (device pointers, no allocation, errors before any launch); 16-byte alignment
@@ -401,6 +403,8 @@ wkv_status gated_delta_decode_step(const void *q, const void *k, const void *v, 
  * its value heads), dv [B][T][H][D] io, domega, dbeta [B][T][H] io, dstate_in [B][H][D][D] fp32
  * or NULL (not computed).  No output may overlap an input, another output or the workspace.
  * T == 0: dstate_in = dstate_out, or zeros.  The same inputs give the same bits (no atomics).
+ * A device-side wait that expires (bf16; about a second, where microseconds are due) leaves NaN
+ * in the dq, dk, domega and dbeta of its 64 tokens.
  */
 size_t gated_delta_backward_workspace_bytes(int B, int T, int H, int HK, int D, wkv_dtype io);
 wkv_status gated_delta_backward(const void *q, const void *k, const void *v, const void *omega,

@@ -57,8 +57,11 @@ struct GdrGrads {
 size_t gdr_backward_f32_bytes(int B, int T, int H);
 cudaError_t launch_gdr_backward_f32(const GdrIn& in, const float* s_in, const GdrGrads& g, void* ws, cudaStream_t st);
 
-// Backward on tensor cores, bf16 I/O.  ws: at least gdr_backward_tc_bytes(B, T, H) bytes.
+// Backward on tensor cores, bf16 I/O.  ws: at least gdr_backward_tc_bytes(B, T, H) bytes.  budget:
+// cycles a wait for the tensor cores may take, after which the block's dq, dk, domega and dbeta
+// are NaN.
 size_t gdr_backward_tc_bytes(int B, int T, int H);
-cudaError_t launch_gdr_backward_tc(const GdrIn& in, const float* s_in, const GdrGrads& g, void* ws, cudaStream_t st);
+cudaError_t launch_gdr_backward_tc(const GdrIn& in, const float* s_in, const GdrGrads& g, void* ws, long long budget,
+                                   cudaStream_t st);
 
 }  // namespace goldwkv

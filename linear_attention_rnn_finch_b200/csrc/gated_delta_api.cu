@@ -161,7 +161,8 @@ wkv_status gated_delta_backward(const void* q, const void* k, const void* v, con
     if (!tokens) return pass_state(dstate_in, dstate_out, sb, st);
     const goldwkv::GdrIn in{q, k, v, omega, beta, scale, B, T, H, HK};
     const goldwkv::GdrGrads g{dy, dstate_out, dq, dk, dv, domega, dbeta, dstate_in};
-    if (io == WKV_BF16) return from_cuda(goldwkv::launch_gdr_backward_tc(in, state_in, g, workspace, st));
+    const long long budget = injected("timeout0") ? 0 : kSpinBudget;
+    if (io == WKV_BF16) return from_cuda(goldwkv::launch_gdr_backward_tc(in, state_in, g, workspace, budget, st));
     return from_cuda(goldwkv::launch_gdr_backward_f32(in, state_in, g, workspace, st));
 }
 

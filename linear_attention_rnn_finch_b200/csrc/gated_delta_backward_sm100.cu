@@ -41,6 +41,7 @@ struct Args {
     // the borders, each [head][count - 1][64][64] fp32
     GdrSegments seg;
     float *a, *s, *d;
+    long long budget;   // cycles a wait of the second launch may take
 };
 
 // Two adjacent accumulators of chain warp `warp` (16 value columns x 16 keys or tokens, from
@@ -265,7 +266,7 @@ gated_delta_bwd_maps_kernel(const __grid_constant__ Args p) {
 // on mma.sync: operand loads kept the shared-memory pipe 60 % busy, 749 us at B8 T4096 H32.)
 constexpr int kOutThreads = 256;
 constexpr uint32_t kTmemCols = 256;
-constexpr long long kSpin = 2000000000LL;   // cycles a wait may take: about a second
+constexpr long long kDrain = 2000000000LL;   // cycles the last wait may take: about a second
 
 struct OutSmem {
     uint8_t q[kTileBytes], k[kTileBytes], dy[kTileBytes];
@@ -343,7 +344,7 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
     uint32_t phase = 0;
     // all wait for the group last issued; bounded, and once late no more waits and no more products
     auto arrived = [&] {
-        if (!s.late && !ptx::mbar_wait(&s.done, phase, kSpin)) s.late = 1;
+        if (!s.late && !ptx::mbar_wait(&s.done, phase, p.budget)) s.late = 1;
         phase ^= 1;
         ptx::tc_fence_after();
     };
@@ -618,13 +619,19 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
         }
         good = ready();   // also: this head's tiles may be overwritten
     }
-    // late: the products last issued may be running still; a second chance to end, and NaN results
+    // late: NaN results; the products last issued may be running still and get a second's time
     if (!good) {
-        (void)ptx::mbar_wait(&s.done, phase ^ 1, kSpin);
+        (void)ptx::mbar_wait(&s.done, phase ^ 1, kDrain);
+        const float nan = __int_as_float(0x7fffffff);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dq[i][e] = dk[i][e] = __int_as_float(0x7fffffff);
+            for (int e = 0; e < 4; ++e) dq[i][e] = dk[i][e] = nan;
+        for (int i = tid; i < per * C; i += kOutThreads)
+            if (t0 + i % C < T) {
+                const size_t o = ((size_t)b * T + t0 + i % C) * H + hk * per + i / C;
+                ((bf16*)p.g.domega)[o] = ((bf16*)p.g.dbeta)[o] = __float2bfloat16_rn(nan);
+            }
     }
     __syncthreads();
     ptx::tc_fence_after();
@@ -669,8 +676,10 @@ size_t gdr_backward_tc_bytes(int B, int T, int H) {
            3 * sizeof(float) * heads * (segments(B, T, H).count - 1) * C * C;
 }
 
-cudaError_t launch_gdr_backward_tc(const GdrIn& in, const float* s_in, const GdrGrads& g, void* ws, cudaStream_t st) {
-    Args a{in, g, s_in, static_cast<uint8_t*>(ws), (in.T + C - 1) / C, segments(in.B, in.T, in.H), nullptr, nullptr, nullptr};
+cudaError_t launch_gdr_backward_tc(const GdrIn& in, const float* s_in, const GdrGrads& g, void* ws, long long budget,
+                                   cudaStream_t st) {
+    Args a{in, g, s_in, static_cast<uint8_t*>(ws), (in.T + C - 1) / C, segments(in.B, in.T, in.H),
+           nullptr, nullptr, nullptr, budget};
     const unsigned heads = (unsigned)(in.B * in.H), last = a.seg.count - 1;
     const size_t smem = sizeof(ChainSmem) + 1024;
     cudaError_t e;

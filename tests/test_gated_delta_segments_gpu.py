@@ -87,3 +87,27 @@ def test_same_bits_replayed():
         g.replay()
         for x, y in zip(want, outs):
             assert torch.equal(x, y)
+
+
+def test_a_wait_that_expires_leaves_nan(monkeypatch):
+    """With no cycles to wait in, the blocks whose products are not done at once are NaN, the
+    others what they are; the call after it is whole again."""
+    p = problem(370, 2, 130, 4, 2, BF16)
+    dy = torch.randn_like(p["v"])
+    want = gw.gated_delta_backward(*args(p), dy, scale=SCALE)
+    monkeypatch.setenv("GOLDWKV_FAULT", "timeout0")
+    got = gw.gated_delta_backward(*args(p), dy, scale=SCALE)
+    torch.cuda.synchronize()
+    monkeypatch.delenv("GOLDWKV_FAULT")
+    assert bool(torch.isnan(got[0]).any())
+    for i in (0, 1, 3, 4):
+        nan = torch.isnan(got[i])
+        assert torch.equal(torch.where(nan, want[i], got[i]), want[i])
+        # whole blocks of 64 tokens: 0-63, 64-127, 128-129
+        for a, b in ((0, 64), (64, 128), (128, 130)):
+            per_head = nan[:, a:b].flatten(3).all(3).all(1) if nan.dim() == 4 else nan[:, a:b].all(1)
+            some = nan[:, a:b].flatten(3).any(3).any(1) if nan.dim() == 4 else nan[:, a:b].any(1)
+            assert torch.equal(per_head, some)
+    assert torch.equal(got[2], want[2]) and torch.equal(got[5], want[5])   # dv, dstate: no such wait
+    for x, y in zip(gw.gated_delta_backward(*args(p), dy, scale=SCALE), want):
+        assert torch.equal(x, y)
