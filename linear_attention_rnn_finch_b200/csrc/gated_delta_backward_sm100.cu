@@ -112,7 +112,7 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh, int s
             if (m + 1 < blocks) {
                 const uint32_t o = (uint32_t)((m + 1) % kStages) * kTileBytes;
                 const Gate next = gate_of(m + 2);
-                prepare_sub<kBack>(s.prep[(m + 1) & 1], s.at[w], sk + o, sq + o, w, gate, p.in.scale, lane);
+                prepare_sub<kBack ? 3 : 0>(s.prep[(m + 1) & 1], s.at[w], sk + o, sq + o, w, gate, p.in.scale, lane);
                 gate = next;
             }
             cp_async_wait<0>();
@@ -182,12 +182,14 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh, int s
                 update_state(S, pr.g_end[j], e, kt + abt);
             } else {
                 // X^T = to_end G^T K^T + dY^T P
-                uint32_t p0[4], p1[4];
+                uint32_t p0[4], p1[4], p2[4];
                 ldsm4t(p0, addr16_bt(pp + j * kTile16, lane));
                 ldsm4t(p1, addr16_bt(pp + (kSubs + j) * kTile16, lane));
+                ldsm4t(p2, addr16_bt(pp + (2 * kSubs + j) * kTile16, lane));
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     scale_cols(f[u], te[u]);
+                    mma(f[u], xv, p2[2 * u], p2[2 * u + 1]);
                     mma(f[u], xv, p1[2 * u], p1[2 * u + 1]);
                     mma(f[u], xv, p0[2 * u], p0[2 * u + 1]);
                     scale_cols(f[u], bt[u]);

@@ -1,5 +1,8 @@
-// Chunked prefill of the gated delta rule, bf16 inputs, on tensor cores (sm_100a).  The algebra
-// and the division of labour are in gated_delta_tiles.cuh.
+// Chunked prefill of the gated delta rule, bf16 inputs, on tensor cores (sm_100a).  The algebra,
+// the division of labour and what bounds it are in gated_delta_tiles.cuh.
+//
+// B8 T4096 H32: 321 us for 540 MB that it has to move (82 us at the memory's rate), token by token
+// on CUDA cores 1771; B1 T65531 H64 over 16 key heads, in two segments: 2.39 ms.
 #include "common.cuh"
 #include "gated_delta.h"
 #include "gated_delta_tiles.cuh"
@@ -74,7 +77,7 @@ __device__ __forceinline__ void walk(const Args& p, int bh, int seg, bool unit, 
                 const uint32_t o = (uint32_t)((n + 1) % kStages) * kTileBytes;
                 const Gate next = load_gate(omega, beta, H, (n + 2) * C + t, T);
                 if ((n + 1) * C + kSub * w < T)
-                    prepare_sub<kOut>(s.prep[(n + 1) & 1], s.at[w], sk + o, sq + o, w, gate, p.in.scale, lane);
+                    prepare_sub<kOut ? 2 : 0>(s.prep[(n + 1) & 1], s.at[w], sk + o, sq + o, w, gate, p.in.scale, lane);
                 gate = next;
             }
             cp_async_wait<0>();

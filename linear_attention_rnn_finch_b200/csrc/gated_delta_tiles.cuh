@@ -8,25 +8,31 @@
 //     S+ = g_16 S + K^T (b to_end E),   to_end_t = e^(L_16 - L_t).
 // 16, not 64: the products with S, Q S, K^T E cost the same per token whatever the length of a
 // sub-chunk, while those with T and P and the inverse grow with it (per 64 tokens and 16 value
-// columns 240 matrix instructions instead of 312, an inverse without block products), and the
-// longer chain of dependent products is hidden by the other CTA of the SM.
+// columns and in two parts 240 matrix instructions instead of 312, an inverse without block
+// products).
 //
 // Four warps (the chain) own 16 value columns each and keep S^T in registers as accumulators
-// (rows value columns, columns key channels; two warps of 32 columns issue less in all, but
-// leave schedulers idle: B8 T4096 H32 423 us against 289).  Everything transposed (F^T = V^T - g S^T K^T,
-// E^T = F^T T^T, ...) each result has the layout of the next product's A operand, so a block
+// (rows value columns, columns key channels; two warps of 32 columns issue less in all, but leave
+// schedulers idle: B8 T4096 H32 423 us against 289).  Everything transposed (F^T = V^T - g S^T K^T,
+// E^T = F^T T^T, ...), each result has the layout of the next product's A operand, so a block
 // passes through them without shared memory or barriers between its products.  Four more warps
 // (the preparation) work one block ahead: they issue the copies of the block after it, and
 // form decays, T and P of one sub-chunk each.  The two halves meet once a block.
 //
-// Operands that are not the caller's bf16 values are kept as two bf16 parts (2^-17 of the value),
-// which takes two products against an exact operand and three against another such pair; T is
-// kept as three, since its rounding comes back with every later sub-chunk where keys are alike
-// and strengths are near two (the state then off by 1e-4 instead of 3e-5 after 150 tokens).
-// Sums are fp32.  mma.sync, not tcgen05: the chain's products are 16 x 16 x 64 and smaller and each
-// needs the one before it, which as tcgen05.mma is a round through shared memory, a barrier, a
-// commit and TMEM loads, several hundred cycles, against 21 cycles for a register-to-register
-// mma.sync (8 cycles a warp scheduler, measured).
+// Operands that are not the caller's bf16 values are kept as sums of bf16 parts: two (2^-17 of the
+// value) where they only lead to bf16 results, and for S as it meets K and Q; three (2^-25) for
+// what comes back in the fp32 state, T, F and the terms added to S, so that it is as exact as fp32
+// sums make it (with two parts of F and of those terms it is off by 3e-6 of its norm instead of
+// 2e-7; with two parts of T, and keys alike with strengths near two, by 1e-4 after 150 tokens).
+// The ten matrix instructions more in 64 take B8 T4096 H32 from 287 to 321 us.  Sums are fp32.
+//
+// mma.sync, not tcgen05: the chain's products are 16 x 16 x 64 and smaller and each needs the one
+// before it, which as tcgen05.mma is a round through shared memory, a barrier, a commit and TMEM
+// loads (a group of 64 x 64 x 64 products takes 1000 cycles and more in the backward's second
+// launch), against 21 cycles for a register-to-register mma.sync, one every 8 a scheduler.  What
+// bounds a chain is its schedulers: an mma.sync keeps the FP32 pipe's dispatch for about 6 of its 8
+// cycles, so the 74 of a sub-chunk and the 400 instructions beside them hardly overlap (1250 cycles
+// a sub-chunk where the tensor pipe needs 600; a second CTA on the SM adds an eighth).
 #pragma once
 
 #include "gated_delta.h"
@@ -54,7 +60,7 @@ __device__ __forceinline__ uint32_t off16(int row, int chunk) {
 // What the preparation hands to the chain for one block.
 struct Prep {
     uint8_t t[3][kSubs][kTile16];    // T in three parts, [t][s]
-    uint8_t p[2][kSubs][kTile16];    // P in two
+    uint8_t p[3][kSubs][kTile16];    // P in two, or three
     float g[C];                      // e^L inside the sub-chunk
     float to_end[C];
     float beta[C];
@@ -95,8 +101,9 @@ __device__ __forceinline__ Gate load_gate(const __nv_bfloat16* omega, const __nv
     return g;
 }
 
-// One warp prepares sub-chunk j of a block.  at: 16 x 20 floats of the warp's own.
-template <bool kP>
+// One warp prepares sub-chunk j of a block, P in kP parts (0: none).  at: 16 x 20 floats of the
+// warp's own.
+template <int kP>
 __device__ __forceinline__ void prepare_sub(Prep& out, float* at, uint32_t kt, uint32_t qt, int j, Gate gate,
                                             float scale, int lane) {
     const int r = lane >> 2, c = 2 * (lane & 3);
@@ -190,11 +197,14 @@ __device__ __forceinline__ void prepare_sub(Prep& out, float* at, uint32_t kt, u
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint32_t a, b;
-                split2(make_float2(qk[n][2 * h], qk[n][2 * h + 1]), a, b);
+                uint32_t a, b, e = 0;
+                const float2 x = make_float2(qk[n][2 * h], qk[n][2 * h + 1]);
+                if (kP == 3) split3(x, a, b, e);
+                else split2(x, a, b);
                 const uint32_t o = off16(r + 8 * h, n) + 2 * c;
                 *reinterpret_cast<uint32_t*>(out.p[0][j] + o) = a;
                 *reinterpret_cast<uint32_t*>(out.p[1][j] + o) = b;
+                if (kP == 3) *reinterpret_cast<uint32_t*>(out.p[2][j] + o) = e;
             }
     }
     __syncwarp();
@@ -204,7 +214,7 @@ __device__ __forceinline__ void prepare_sub(Prep& out, float* at, uint32_t kt, u
 // T's first part.  The smallest terms first, in two chains of sums.
 template <bool kTrans = false>
 __device__ __forceinline__ void times_t(float (&e)[2][4], const float (&x)[2][4], uint32_t t, int lane) {
-    uint32_t b0[4], b1[4], b2[4], hi[4], lo[4];
+    uint32_t b0[4], b1[4], b2[4], a0[4], a1[4], a2[4];
     const uint32_t at = kTrans ? addr16_bt(t, lane) : addr16_b(t, lane);
     if (kTrans) {
         ldsm4t(b0, at);
@@ -216,19 +226,22 @@ __device__ __forceinline__ void times_t(float (&e)[2][4], const float (&x)[2][4]
         ldsm4(b2, at + 2 * kSubs * kTile16);
     }
     float f[2][4];
-    split_a(hi, lo, x[0], x[1]);
+    split_a3(a0, a1, a2, x[0], x[1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        mma0(e[i], hi, b2[2 * i], b2[2 * i + 1]);
-        mma0(f[i], lo, b1[2 * i], b1[2 * i + 1]);
+        mma0(e[i], a0, b2[2 * i], b2[2 * i + 1]);
+        mma0(f[i], a2, b0[2 * i], b0[2 * i + 1]);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        mma(e[i], hi, b1[2 * i], b1[2 * i + 1]);
-        mma(f[i], lo, b0[2 * i], b0[2 * i + 1]);
+        mma(e[i], a1, b1[2 * i], b1[2 * i + 1]);
+        mma(f[i], a1, b0[2 * i], b0[2 * i + 1]);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) mma(e[i], hi, b0[2 * i], b0[2 * i + 1]);
+    for (int i = 0; i < 2; ++i) {
+        mma(e[i], a0, b1[2 * i], b1[2 * i + 1]);
+        mma(f[i], a0, b0[2 * i], b0[2 * i + 1]);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -262,8 +275,8 @@ __device__ __forceinline__ void store_state(float* dst, const float (&S)[8][4], 
 
 // S^T = factor S^T + X^T K: X^T as accumulators; kt: addr_bt of K's 16 rows at chunk 0.
 __device__ __forceinline__ void update_state(float (&S)[8][4], float factor, const float (&x)[2][4], uint32_t kt) {
-    uint32_t hi[4], lo[4];
-    split_a(hi, lo, x[0], x[1]);
+    uint32_t a0[4], a1[4], a2[4];
+    split_a3(a0, a1, a2, x[0], x[1]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t kb[4];
@@ -272,10 +285,12 @@ __device__ __forceinline__ void update_state(float (&S)[8][4], float factor, con
         for (int u = 0; u < 2; ++u) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) S[2 * i + u][e] *= factor;
-            mma(S[2 * i + u], lo, kb[2 * u], kb[2 * u + 1]);
+            mma(S[2 * i + u], a2, kb[2 * u], kb[2 * u + 1]);
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) mma(S[2 * i + u], hi, kb[2 * u], kb[2 * u + 1]);
+        for (int u = 0; u < 2; ++u) mma(S[2 * i + u], a1, kb[2 * u], kb[2 * u + 1]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) mma(S[2 * i + u], a0, kb[2 * u], kb[2 * u + 1]);
     }
 }
 

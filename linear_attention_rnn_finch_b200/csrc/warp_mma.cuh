@@ -81,6 +81,20 @@ __device__ __forceinline__ void split_a(uint32_t (&hi)[4], uint32_t (&lo)[4], co
     split2(make_float2(y[2], y[3]), hi[3], lo[3]);
 }
 
+// x = a + b + c within 2^-25 |x|.
+__device__ __forceinline__ void split3(float2 x, uint32_t& a, uint32_t& b, uint32_t& c) {
+    a = tiles::pack2(x.x, x.y);
+    const float2 d = __fadd2_rn(x, make_float2(-__uint_as_float(a << 16), -__uint_as_float(a & 0xFFFF0000u)));
+    split2(d, b, c);
+}
+__device__ __forceinline__ void split_a3(uint32_t (&a)[4], uint32_t (&b)[4], uint32_t (&c)[4], const float (&x)[4],
+                                         const float (&y)[4]) {
+    split3(make_float2(x[0], x[1]), a[0], b[0], c[0]);
+    split3(make_float2(x[2], x[3]), a[1], b[1], c[1]);
+    split3(make_float2(y[0], y[1]), a[2], b[2], c[2]);
+    split3(make_float2(y[2], y[3]), a[3], b[3], c[3]);
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
