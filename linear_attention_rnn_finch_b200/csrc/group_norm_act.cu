@@ -98,8 +98,8 @@ __device__ __forceinline__ float act(float x, bool silu) { return silu ? x * sig
 template <typename IO>
 __device__ __forceinline__ float2 act_grad(float x, bool silu) {
     if (!silu) return make_float2(x, 1.f);
-    const float s = sigmoid<IO>(x);
-    return make_float2(x * s, s * fmaf(x, 1.f - s, 1.f));
+    const float s = sigmoid<IO>(x), xs = x * s;
+    return make_float2(xs, fmaf(xs, 1.f - s, s));
 }
 
 // sum over the `lanes` (a power of two) adjacent lanes of a group
@@ -451,6 +451,130 @@ group_norm_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
             }
         }
     }
+}
+
+// Groups of 8 kL channels, kL a power of two: every lane of a set holds one vector, so that
+// nothing is left to test in the loop (a set whose turns end leaves; the shuffles are among a
+// set's lanes only), and the sums' steps are known.  The gradient issues 49 instructions a value
+// instead of 57 and takes 32768 rows of 2048 from 156 to 136 us, the norm itself from 76 to 69.
+template <int kL>
+__device__ __forceinline__ float set_sum(float x, unsigned lanes) {
+#pragma unroll
+    for (int o = kL >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(lanes, x, o);
+    return x;
+}
+template <int kL>
+__device__ __forceinline__ unsigned set_lanes() {
+    return kL == 32 ? 0xffffffffu : ((1u << (kL & 31)) - 1) << (threadIdx.x & 31 & ~(kL - 1));
+}
+
+template <typename IO, int kL, bool kGate, bool kSilu>
+__global__ void __launch_bounds__(kThreads)
+group_norm_full_rows_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
+                            const float* __restrict__ gamma, const float* __restrict__ beta, float eps,
+                            IO* __restrict__ y, RowShape s) {
+    constexpr int V = 8;
+    const RowSet set = row_set(s);
+    if (!set.in) return;
+    const unsigned lanes = set_lanes<kL>();
+    const int c0 = set.g * s.per + set.l * V;
+    constexpr float inv_n = 1.f / (kL * V);
+    float ga[V], be[V];
+    load<V>(gamma + c0, ga);
+    load<V>(beta + c0, be);
+    const size_t stride = (size_t)s.streams * s.C;
+    size_t o = (size_t)set.n * s.C + c0;
+    int left = (int)((s.rows - set.n + s.streams - 1) / s.streams);   // rows of this set
+    Raw<IO, V> rx = load_raw<IO, V>(x + o), rg;
+    if (kGate) rg = load_raw<IO, V>(gate + o);
+    for (; left > 0; --left, o += stride) {
+        float v[V], gt[V], sum = 0.f, sq = 0.f;
+        convert(rx, v);
+        if (kGate) convert(rg, gt);
+        if (left > 1) {
+            rx = load_raw<IO, V>(x + o + stride);
+            if (kGate) rg = load_raw<IO, V>(gate + o + stride);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum += v[e];
+        const float mean = set_sum<kL>(sum, lanes) * inv_n;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            v[e] -= mean;
+            sq = fmaf(v[e], v[e], sq);
+        }
+        const float r = rsqrtf(set_sum<kL>(sq, lanes) * inv_n + eps);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float z = fmaf(v[e] * r, ga[e], be[e]);
+            v[e] = kGate ? z * act<IO>(gt[e], kSilu) : act<IO>(z, kSilu);
+        }
+        store<V>(y + o, v);
+    }
+}
+
+template <typename IO, int kL, bool kGate, bool kSilu>
+__global__ void __launch_bounds__(kThreads, sizeof(IO) == 4 ? 2 : 3)
+group_norm_full_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
+                                const float* __restrict__ gamma, const float* __restrict__ beta,
+                                float eps, const IO* __restrict__ dy, IO* __restrict__ dx,
+                                IO* __restrict__ dgate, float* __restrict__ part, RowShape s) {
+    constexpr int V = 8;
+    const RowSet set = row_set(s);
+    if (!set.in) return;
+    const unsigned lanes = set_lanes<kL>();
+    const int c0 = set.g * s.per + set.l * V;
+    constexpr float inv_n = 1.f / (kL * V);
+    float ga[V], be[V], dga[V], dbe[V];
+    load<V>(gamma + c0, ga);
+    load<V>(beta + c0, be);
+#pragma unroll
+    for (int e = 0; e < V; ++e) dga[e] = dbe[e] = 0.f;
+    const size_t stride = (size_t)s.streams * s.C;
+    size_t o = (size_t)set.n * s.C + c0;
+    int left = (int)((s.rows - set.n + s.streams - 1) / s.streams);
+    Raw<IO, V> rx = load_raw<IO, V>(x + o), rd = load_raw<IO, V>(dy + o), rg;
+    if (kGate) rg = load_raw<IO, V>(gate + o);
+    for (; left > 0; --left, o += stride) {
+        float v[V], d[V], gt[V], sum = 0.f, sq = 0.f, s1 = 0.f, s2 = 0.f;
+        convert(rx, v);
+        convert(rd, d);
+        if (kGate) convert(rg, gt);
+        if (left > 1) {
+            rx = load_raw<IO, V>(x + o + stride);
+            rd = load_raw<IO, V>(dy + o + stride);
+            if (kGate) rg = load_raw<IO, V>(gate + o + stride);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum += v[e];
+        const float mean = set_sum<kL>(sum, lanes) * inv_n;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            v[e] -= mean;
+            sq = fmaf(v[e], v[e], sq);
+        }
+        const float r = rsqrtf(set_sum<kL>(sq, lanes) * inv_n + eps);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            v[e] *= r;
+            const float dz = value_grad<IO, kGate>(v[e], ga[e], be[e], d[e], gt[e], kSilu);
+            dga[e] = fmaf(dz, v[e], dga[e]);
+            dbe[e] += dz;
+            d[e] = dz * ga[e];
+            s1 += d[e];
+            s2 = fmaf(d[e], v[e], s2);
+        }
+        if (kGate) store<V>(dgate + o, gt);
+        s1 = set_sum<kL>(s1, lanes) * inv_n * r;
+        s2 = set_sum<kL>(s2, lanes) * inv_n * r;
+#pragma unroll
+        for (int e = 0; e < V; ++e) d[e] = fmaf(-v[e], s2, fmaf(d[e], r, -s1));
+        store<V>(dx + o, d);
+    }
+    // partial rows: dgamma then dbeta, [streams][2][C]
+    float* pg = part + (size_t)set.n * 2 * s.C + c0;
+    store<V>(pg, dga);
+    store<V>(pg + s.C, dbe);
 }
 
 // dgamma[c], dbeta[c] = the sums of `rows` partial rows ([rows][2][C]), in a fixed order: 32
@@ -964,11 +1088,35 @@ cudaError_t with_constants(const GroupNorm& a, const Tiling& t, F f) {
     return t.V == 8 ? gated(integral_constant<int, 8>{}) : gated(integral_constant<int, 1>{});
 }
 
+// f(lanes of a set, gate, silu) as compile-time constants, where a group is exactly a power of two
+// of vectors of 8, up to 32; false otherwise.
+template <typename F>
+bool full_rows(const GroupNorm& a, const RowShape& s, F f) {
+    using std::integral_constant;
+    if (s.per % 8 != 0 || s.units != s.lanes) return false;
+    auto act = [&](auto l, auto gate) { a.silu ? f(l, gate, std::true_type{}) : f(l, gate, std::false_type{}); };
+    auto run = [&](auto l) { a.gate ? act(l, std::true_type{}) : act(l, std::false_type{}); };
+    switch (s.lanes) {
+    case 1: run(integral_constant<int, 1>{}); break;
+    case 2: run(integral_constant<int, 2>{}); break;
+    case 4: run(integral_constant<int, 4>{}); break;
+    case 8: run(integral_constant<int, 8>{}); break;
+    case 16: run(integral_constant<int, 16>{}); break;
+    default: run(integral_constant<int, 32>{}); break;
+    }
+    return true;
+}
+
 template <typename IO>
 cudaError_t forward_io(const GroupNorm& a, void* y, void* ws, cudaStream_t st) {
     if (a.L == 1) {
         const RowShape s = row_shape(a.N, a.C, a.groups, kFwdCtas);
         const int u = row_units(s);
+        if (full_rows(a, s, [&](auto l, auto gate, auto silu) {
+                group_norm_full_rows_kernel<IO, l(), gate(), silu()><<<row_ctas(s), kThreads, 0, st>>>(
+                    (const IO*)a.x, (const IO*)a.gate, a.gamma, a.beta, a.eps, (IO*)y, s);
+            }))
+            return cudaGetLastError();
         if (s.per % 8 == 0)
             return u == 1 ? rows_fwd<IO, 8, 1>(a, y, s, st) : u == 2 ? rows_fwd<IO, 8, 2>(a, y, s, st)
                  : u == 4 ? rows_fwd<IO, 8, 4>(a, y, s, st) : rows_fwd<IO, 8, 0>(a, y, s, st);
@@ -990,7 +1138,13 @@ cudaError_t backward_io(const GroupNorm& a, const void* dy, void* dx, float* dga
         const int u = row_units(s);
         float* part = static_cast<float*>(ws);
         cudaError_t e;
-        if (s.per % 8 == 0)
+        if (full_rows(a, s, [&](auto l, auto gate, auto silu) {
+                group_norm_full_rows_bwd_kernel<IO, l(), gate(), silu()><<<row_ctas(s), kThreads, 0, st>>>(
+                    (const IO*)a.x, (const IO*)a.gate, a.gamma, a.beta, a.eps, (const IO*)dy, (IO*)dx, (IO*)dgate,
+                    part, s);
+            }))
+            e = cudaGetLastError();
+        else if (s.per % 8 == 0)
             e = u == 1 ? rows_bwd<IO, 8, 1>(a, dy, dx, dgate, part, s, st)
               : u == 2 ? rows_bwd<IO, 8, 2>(a, dy, dx, dgate, part, s, st)
                        : rows_bwd<IO, 8, 0>(a, dy, dx, dgate, part, s, st);   // 4 would spill
