@@ -22,35 +22,37 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
 }
 
 // ------------------------------------------------------------------ prefill
-// Value columns are independent, so a CTA owns 32 of a head's 64 (grid B*H x 2): twice the
-// CTAs when there are few heads.  Four adjacent lanes share a column, 16 state rows each in
-// registers; two xor-shuffles finish the sums over rows.  The chain from one token to the
-// next is those sums, e and one FMA per state entry, about 100 cycles, and bounds a call with
-// few heads; with many, the 64 FMAs a thread and token do.  Tokens come through shared memory
-// in tiles of 16, the next tile's loads issued before the present one is walked.
+// Value columns are independent.  Four adjacent lanes share kJ columns, 16 state rows each in
+// registers; two xor-shuffles finish the sums over rows.  A CTA of 128 threads owns 32 kJ columns
+// of a head: 32, grid B*H x 2, when there are few heads, where the chain from one token to the next
+// bounds the call (the sums, e and one FMA per state entry, 300 cycles with a warp a scheduler);
+// 64, grid B*H, from one CTA an SM on, where reading q and k from shared memory bounds it and two
+// columns a thread read them once (B8 T1024 H32: 332 us against 409; B4 T2048 H16 433 against 326).  Tokens come through shared
+// memory in tiles of 16, the next tile's loads issued before the present one is walked.
 constexpr int kTile = 16;
-constexpr int kCols = 32;
 constexpr int kThreads = 128;
 constexpr int kRow = D + 4;   // padded token row: the k . q sums read a column of rows
 
+template <int kJ>
 struct Stage {
     float q[kTile][kRow];
     float k[kTile][kRow];
-    float v[kTile][kCols];
+    float v[kTile][32 * kJ];
     float w[kTile], b[kTile], kq[kTile];
 };
 
+template <int kJ>
 __global__ void __launch_bounds__(kThreads)
 gated_delta_recurrent_kernel(const float* __restrict__ q, const float* __restrict__ k,
                              const float* __restrict__ v, const float* __restrict__ omega,
                              const float* __restrict__ beta, float scale, const float* s_in,
                              float* s_out, float* __restrict__ y, int T, int H, int HK) {
-    __shared__ __align__(16) Stage stage[2];
+    __shared__ __align__(16) Stage<kJ> stage[2];
     const int bh = blockIdx.x, b = bh / H, h = bh - b * H, hk = h / (H / HK);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int part = lane & 3;                    // rows 4 (4 m + part) + {0..3}, m = 0..3
-    const int jl = warp * 8 + (lane >> 2);        // column within the CTA
-    const int j0 = blockIdx.y * kCols;
+    const int jl = kJ * (warp * 8 + (lane >> 2)); // first column within the CTA
+    const int j0 = blockIdx.y * 32 * kJ;
 
     const float* qp = q + ((size_t)b * T * HK + hk) * D;     // token t: + t * HK * D
     const float* kp = k + ((size_t)b * T * HK + hk) * D;
@@ -60,15 +62,17 @@ gated_delta_recurrent_kernel(const float* __restrict__ q, const float* __restric
     float* yp = y + ((size_t)b * T * H + h) * D + j0 + jl;
     const size_t kstep = (size_t)HK * D, vstep = (size_t)H * D;
 
-    float S[16];
+    float S[kJ][16];
     const float* s0 = s_in ? s_in + (size_t)bh * D * D + j0 + jl : nullptr;
 #pragma unroll
     for (int m = 0; m < 16; ++m)
-        S[m] = s0 ? s0[(size_t)(16 * (m >> 2) + 4 * part + (m & 3)) * D] : 0.f;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j)
+            S[j][m] = s0 ? s0[(size_t)(16 * (m >> 2) + 4 * part + (m & 3)) * D + j] : 0.f;
 
-    // a thread stages 4 channels of tokens tid/16 and tid/16 + 8 of q and k, 4 of token tid/8 of v
+    // a thread stages 4 channels of tokens tid/16 and tid/16 + 8 of q and k, 4 kJ of token tid/8 of v
     const int tq = tid >> 4, cq = 4 * (tid & 15), tv = tid >> 3, cv = 4 * (tid & 7);
-    float4 rq[2], rk[2], rv;
+    float4 rq[2], rk[2], rv[kJ];
     float rw = 0.f, rb = 0.f;
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
     auto fetch = [&](int t0) {
@@ -78,16 +82,17 @@ gated_delta_recurrent_kernel(const float* __restrict__ q, const float* __restric
             rq[i] = t < T ? load4(qp + t * kstep + cq) : zero;
             rk[i] = t < T ? load4(kp + t * kstep + cq) : zero;
         }
-        rv = t0 + tv < T ? load4(vp + (t0 + tv) * vstep + cv) : zero;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) rv[j] = t0 + tv < T ? load4(vp + (t0 + tv) * vstep + cv + 32 * j) : zero;
         if (tid < kTile && t0 + tid < T) {
-            rw = to_f32(op[(size_t)(t0 + tid) * H]);
-            rb = to_f32(bp[(size_t)(t0 + tid) * H]);
+            rw = op[(size_t)(t0 + tid) * H];
+            rb = bp[(size_t)(t0 + tid) * H];
         }
     };
     fetch(0);
     const int tiles = (T + kTile - 1) / kTile;
     for (int n = 0; n < tiles; ++n) {
-        Stage& s = stage[n & 1];
+        Stage<kJ>& s = stage[n & 1];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             *reinterpret_cast<float4*>(&s.q[tq + 8 * i][cq]) = rq[i];
@@ -98,7 +103,8 @@ gated_delta_recurrent_kernel(const float* __restrict__ q, const float* __restric
             for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
             if ((lane & 15) == 0) s.kq[tq + 8 * i] = d;
         }
-        *reinterpret_cast<float4*>(&s.v[tv][cv]) = rv;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) *reinterpret_cast<float4*>(&s.v[tv][cv + 32 * j]) = rv[j];
         if (tid < kTile) {
             s.w[tid] = decay_from_logit(rw);
             s.b[tid] = rb;
@@ -108,38 +114,50 @@ gated_delta_recurrent_kernel(const float* __restrict__ q, const float* __restric
         const int cnt = min(kTile, T - n * kTile);
         for (int t = 0; t < cnt; ++t) {
             float4 kk[4];
-            float a[4], c[4];
+            float a[kJ][4], c[kJ][4];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 kk[m] = *reinterpret_cast<const float4*>(&s.k[t][16 * m + 4 * part]);
                 const float4 qq = *reinterpret_cast<const float4*>(&s.q[t][16 * m + 4 * part]);
-                const float4 x = make_float4(S[4 * m], S[4 * m + 1], S[4 * m + 2], S[4 * m + 3]);
-                a[m] = dot4(kk[m], x, 0.f);
-                c[m] = dot4(qq, x, 0.f);
-            }
-            float as = (a[0] + a[1]) + (a[2] + a[3]), cs = (c[0] + c[1]) + (c[2] + c[3]);
-            as += __shfl_xor_sync(0xffffffffu, as, 1);
-            cs += __shfl_xor_sync(0xffffffffu, cs, 1);
-            as += __shfl_xor_sync(0xffffffffu, as, 2);
-            cs += __shfl_xor_sync(0xffffffffu, cs, 2);
-            const float w = s.w[t];
-            const float be = s.b[t] * fmaf(-w, as, s.v[t][jl]);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                S[4 * m] = fmaf(kk[m].x, be, w * S[4 * m]);
-                S[4 * m + 1] = fmaf(kk[m].y, be, w * S[4 * m + 1]);
-                S[4 * m + 2] = fmaf(kk[m].z, be, w * S[4 * m + 2]);
-                S[4 * m + 3] = fmaf(kk[m].w, be, w * S[4 * m + 3]);
+                for (int j = 0; j < kJ; ++j) {
+                    const float4 x = make_float4(S[j][4 * m], S[j][4 * m + 1], S[j][4 * m + 2], S[j][4 * m + 3]);
+                    a[j][m] = dot4(kk[m], x, 0.f);
+                    c[j][m] = dot4(qq, x, 0.f);
+                }
             }
+            const float w = s.w[t];
+            float be[kJ], out[kJ];
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+                float as = (a[j][0] + a[j][1]) + (a[j][2] + a[j][3]), cs = (c[j][0] + c[j][1]) + (c[j][2] + c[j][3]);
+                as += __shfl_xor_sync(0xffffffffu, as, 1);
+                cs += __shfl_xor_sync(0xffffffffu, cs, 1);
+                as += __shfl_xor_sync(0xffffffffu, as, 2);
+                cs += __shfl_xor_sync(0xffffffffu, cs, 2);
+                be[j] = s.b[t] * fmaf(-w, as, s.v[t][jl + j]);
+                out[j] = scale * fmaf(s.kq[t], be[j], w * cs);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    S[j][4 * m] = fmaf(kk[m].x, be[j], w * S[j][4 * m]);
+                    S[j][4 * m + 1] = fmaf(kk[m].y, be[j], w * S[j][4 * m + 1]);
+                    S[j][4 * m + 2] = fmaf(kk[m].z, be[j], w * S[j][4 * m + 2]);
+                    S[j][4 * m + 3] = fmaf(kk[m].w, be[j], w * S[j][4 * m + 3]);
+                }
             if (part == 0)
-                yp[(size_t)(n * kTile + t) * vstep] = scale * fmaf(s.kq[t], be, w * cs);
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) yp[(size_t)(n * kTile + t) * vstep + j] = out[j];
         }
     }
     if (s_out) {
         float* so = s_out + (size_t)bh * D * D + j0 + jl;
 #pragma unroll
         for (int m = 0; m < 16; ++m)
-            so[(size_t)(16 * (m >> 2) + 4 * part + (m & 3)) * D] = S[m];
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) so[(size_t)(16 * (m >> 2) + 4 * part + (m & 3)) * D + j] = S[j][m];
     }
 }
 
@@ -260,9 +278,14 @@ cudaError_t decode_io(const GdrIn& in, float* state, void* y, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_gdr_recurrent(const GdrIn& in, const float* s_in, float* s_out, void* y, cudaStream_t st) {
-    gated_delta_recurrent_kernel<<<dim3((unsigned)(in.B * in.H), D / kCols), kThreads, 0, st>>>(
-        (const float*)in.q, (const float*)in.k, (const float*)in.v, (const float*)in.omega,
-        (const float*)in.beta, in.scale, s_in, s_out, (float*)y, in.T, in.H, in.HK);
+    const unsigned heads = (unsigned)(in.B * in.H);
+    auto run = [&](auto kernel, unsigned parts) {
+        kernel<<<dim3(heads, parts), kThreads, 0, st>>>(
+            (const float*)in.q, (const float*)in.k, (const float*)in.v, (const float*)in.omega,
+            (const float*)in.beta, in.scale, s_in, s_out, (float*)y, in.T, in.H, in.HK);
+    };
+    if (heads >= 148) run(gated_delta_recurrent_kernel<2>, 1);   // a CTA an SM
+    else run(gated_delta_recurrent_kernel<1>, 2);
     return cudaGetLastError();
 }
 

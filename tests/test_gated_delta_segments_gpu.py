@@ -111,3 +111,16 @@ def test_a_wait_that_expires_leaves_nan(monkeypatch):
     assert torch.equal(got[2], want[2]) and torch.equal(got[5], want[5])   # dv, dstate: no such wait
     for x, y in zip(gw.gated_delta_backward(*args(p), dy, scale=SCALE), want):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+@pytest.mark.parametrize("B,H,HK,T", [(37, 4, 2, 35), (149, 1, 1, 17)])
+def test_prefill_of_many_heads(B, H, HK, T, dtype):
+    """From 148 heads on, where fp32 takes all 64 value columns in one block of threads."""
+    check_prefill(problem(380, B, T, H, HK, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_backward_of_many_heads(dtype):
+    """From 74 heads on, where fp32 takes all 64 value columns in one block of threads."""
+    check_backward(problem(390, 19, 70, 4, 2, dtype), dtype)
