@@ -75,7 +75,9 @@ struct ChainSmem {
 
 // Segment `seg` of head bh from the state (or gradient) `from` (null: zero; `unit`: the identity,
 // with v = 0).  kStore: what the second launch reads, and dV; otherwise only the final matrix.
-template <bool kBack, bool kStore>
+// kExact: what comes back is kept in three parts; the forward chain's E and S end in bf16 gradients
+// and do with two, but for A, which carries the state's fp32 gradient too.
+template <bool kBack, bool kStore, bool kExact>
 __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh, int seg, bool unit, const float* from,
                                       float* to) {
     const int H = p.in.H, HK = p.in.HK, b = bh / H, h = bh - b * H, hk = h / (H / HK);
@@ -175,11 +177,11 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh, int s
             if (!kBack) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) value_minus(f[u], g[u], xv[2 * u], xv[2 * u + 1]);
-                times_t(e, f, pt + j * kTile16, lane);
+                times_t<kExact>(e, f, pt + j * kTile16, lane);
                 if (kStore) put(wb + kMat, e[0], e[1], j, warp, lane, s.y[warp]);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) scale_cols(e[u], make_float2(bt[u].x * te[u].x, bt[u].y * te[u].y));
-                update_state(S, pr.g_end[j], e, kt + abt);
+                update_state<kExact>(S, pr.g_end[j], e, kt + abt);
             } else {
                 // X^T = to_end G^T K^T + dY^T P
                 uint32_t p0[4], p1[4], p2[4];
@@ -194,7 +196,7 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh, int s
                     mma(f[u], xv, p0[2 * u], p0[2 * u + 1]);
                     scale_cols(f[u], bt[u]);
                 }
-                times_t<true>(e, f, pt + j * kTile16, lane);
+                times_t<kExact, true>(e, f, pt + j * kTile16, lane);
                 if (kStore)
                     store_tokens(dv + (size_t)(t0 + row) * H * C, (size_t)H * C, T - t0 - row, e, s.y[warp], lane);
                 if (kStore) put(wb + kMat, e[0], e[1], j, warp, lane, s.y[warp]);
@@ -209,8 +211,8 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh, int s
                     scale_cols(f[u], make_float2(p.in.scale * g[u].x, p.in.scale * g[u].y));
                     scale_cols(e[u], make_float2(-g[u].x, -g[u].y));
                 }
-                update_state(S, pr.g_end[j], f, kt + abt + (sq - sk));
-                update_state(S, 1.f, e, kt + abt);
+                update_state<kExact>(S, pr.g_end[j], f, kt + abt + (sq - sk));
+                update_state<kExact>(S, 1.f, e, kt + abt);
             }
         }
         __syncthreads();
@@ -228,11 +230,11 @@ gated_delta_bwd_chains_kernel(const __grid_constant__ Args p) {
     const int i = back ? blockIdx.x : blockIdx.x - half, bh = i / n, seg = i - bh * n;
     const size_t at = (size_t)bh * C * C, border = (size_t)bh * last;
     if (back)
-        chain<true, true>(s, p, bh, seg, false,
+        chain<true, true, true>(s, p, bh, seg, false,
                           seg < last ? p.d + (border + seg) * C * C : p.g.ds_out ? p.g.ds_out + at : nullptr,
                           seg == 0 && p.g.ds_in ? p.g.ds_in + at : nullptr);
     else
-        chain<false, true>(s, p, bh, seg, false,
+        chain<false, true, false>(s, p, bh, seg, false,
                            seg > 0 ? p.s + (border + seg - 1) * C * C : p.s_in ? p.s_in + at : nullptr, nullptr);
 }
 
@@ -246,15 +248,15 @@ gated_delta_bwd_maps_kernel(const __grid_constant__ Args p) {
     const size_t at = (size_t)bh * C * C, border = (size_t)bh * last;
     if (i < last) {
         const int seg = i + 1;
-        chain<true, false>(s, p, bh, seg, false, seg == last && p.g.ds_out ? p.g.ds_out + at : nullptr,
+        chain<true, false, true>(s, p, bh, seg, false, seg == last && p.g.ds_out ? p.g.ds_out + at : nullptr,
                            p.d + (border + i) * C * C);
     } else if (i < 2 * last) {
         const int seg = i - last;
-        chain<false, false>(s, p, bh, seg, false, seg == 0 && p.s_in ? p.s_in + at : nullptr,
+        chain<false, false, false>(s, p, bh, seg, false, seg == 0 && p.s_in ? p.s_in + at : nullptr,
                             p.s + (border + seg) * C * C);
     } else {
         const int seg = i - 2 * last + 1;
-        chain<false, false>(s, p, bh, seg, true, nullptr, p.a + (border + seg) * C * C);
+        chain<false, false, true>(s, p, bh, seg, true, nullptr, p.a + (border + seg) * C * C);
     }
 }
 

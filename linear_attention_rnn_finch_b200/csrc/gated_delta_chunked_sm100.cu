@@ -142,7 +142,7 @@ __device__ __forceinline__ void walk(const Args& p, int bh, int seg, bool unit, 
                 value_minus(f[u], g[u], vv[2 * u], vv[2 * u + 1]);
             }
             float e[2][4];
-            times_t(e, f, pt + j * kTile16, lane);
+            times_t<true>(e, f, pt + j * kTile16, lane);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 scale_cols(e[u], *reinterpret_cast<const float2*>(&pr.beta[row + 8 * u + c]));
@@ -150,7 +150,7 @@ __device__ __forceinline__ void walk(const Args& p, int bh, int seg, bool unit, 
                 for (int x = 0; x < 4; ++x) f[u][x] = e[u][x];
                 scale_cols(f[u], *reinterpret_cast<const float2*>(&pr.to_end[row + 8 * u + c]));
             }
-            update_state(S, pr.g_end[j], f, kt + abt);
+            update_state<true>(S, pr.g_end[j], f, kt + abt);
             if (kOut) {
                 // Y^T = scale g (S^T Q^T) + (b E)^T P^T
                 uint32_t p0[4], p1[4], hi[4], lo[4];

@@ -210,9 +210,10 @@ __device__ __forceinline__ void prepare_sub(Prep& out, float* at, uint32_t kt, u
     __syncwarp();
 }
 
-// E^T = F^T T^T (kTrans: F^T T) for a chain warp: F^T as accumulators, `t` the sub-chunk's tile of
-// T's first part.  The smallest terms first, in two chains of sums.
-template <bool kTrans = false>
+// E^T = F^T T^T (kTrans: F^T T) for a chain warp: F^T as accumulators, taken in three parts (kExact)
+// or two; `t` the sub-chunk's tile of T's first part.  The smallest terms first, in two chains of
+// sums.
+template <bool kExact, bool kTrans = false>
 __device__ __forceinline__ void times_t(float (&e)[2][4], const float (&x)[2][4], uint32_t t, int lane) {
     uint32_t b0[4], b1[4], b2[4], a0[4], a1[4], a2[4];
     const uint32_t at = kTrans ? addr16_bt(t, lane) : addr16_b(t, lane);
@@ -226,16 +227,18 @@ __device__ __forceinline__ void times_t(float (&e)[2][4], const float (&x)[2][4]
         ldsm4(b2, at + 2 * kSubs * kTile16);
     }
     float f[2][4];
-    split_a3(a0, a1, a2, x[0], x[1]);
+    if (kExact) split_a3(a0, a1, a2, x[0], x[1]);
+    else split_a(a0, a1, x[0], x[1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         mma0(e[i], a0, b2[2 * i], b2[2 * i + 1]);
-        mma0(f[i], a2, b0[2 * i], b0[2 * i + 1]);
+        if (kExact) mma0(f[i], a2, b0[2 * i], b0[2 * i + 1]);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         mma(e[i], a1, b1[2 * i], b1[2 * i + 1]);
-        mma(f[i], a1, b0[2 * i], b0[2 * i + 1]);
+        if (kExact) mma(f[i], a1, b0[2 * i], b0[2 * i + 1]);
+        else mma0(f[i], a1, b0[2 * i], b0[2 * i + 1]);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -273,10 +276,13 @@ __device__ __forceinline__ void store_state(float* dst, const float (&S)[8][4], 
         for (int e = 0; e < 4; ++e) dst[(8 * i + c + (e & 1)) * C + 16 * cw + r + 8 * (e >> 1)] = S[i][e];
 }
 
-// S^T = factor S^T + X^T K: X^T as accumulators; kt: addr_bt of K's 16 rows at chunk 0.
+// S^T = factor S^T + X^T K: X^T as accumulators, taken in three parts (kExact) or two; kt: addr_bt of
+// K's 16 rows at chunk 0.
+template <bool kExact>
 __device__ __forceinline__ void update_state(float (&S)[8][4], float factor, const float (&x)[2][4], uint32_t kt) {
     uint32_t a0[4], a1[4], a2[4];
-    split_a3(a0, a1, a2, x[0], x[1]);
+    if (kExact) split_a3(a0, a1, a2, x[0], x[1]);
+    else split_a(a0, a1, x[0], x[1]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t kb[4];
@@ -285,7 +291,7 @@ __device__ __forceinline__ void update_state(float (&S)[8][4], float factor, con
         for (int u = 0; u < 2; ++u) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) S[2 * i + u][e] *= factor;
-            mma(S[2 * i + u], a2, kb[2 * u], kb[2 * u + 1]);
+            if (kExact) mma(S[2 * i + u], a2, kb[2 * u], kb[2 * u + 1]);
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) mma(S[2 * i + u], a1, kb[2 * u], kb[2 * u + 1]);
