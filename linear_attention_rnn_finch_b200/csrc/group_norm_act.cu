@@ -799,7 +799,7 @@ group_norm_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
         r[e] *= st.y;
     });
     const size_t base = ((size_t)p.n * t.L) * t.C + p.c0;
-#pragma unroll 2
+#pragma unroll 4
     for (long l = p.l0; l < p.l1; l += t.lanes) {
         const size_t o = base + (size_t)l * t.C;
         float v[V], gt[V];
@@ -841,7 +841,7 @@ group_norm_bwd_sums_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
             r[e] = st.y;
         });
         const size_t base = ((size_t)p.n * t.L) * t.C + p.c0;
-#pragma unroll 2
+#pragma unroll 4
         for (long l = p.l0; l < p.l1; l += t.lanes) {
             const size_t o = base + (size_t)l * t.C;
             float v[V], d[V], gt[V];
@@ -937,7 +937,7 @@ group_norm_bwd_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gat
         s2[e] = su.y;
     });
     const size_t base = ((size_t)p.n * t.L) * t.C + p.c0;
-#pragma unroll 2
+#pragma unroll 4
     for (long l = p.l0; l < p.l1; l += t.lanes) {
         const size_t o = base + (size_t)l * t.C;
         float v[V], d[V], gt[V];
