@@ -48,20 +48,21 @@ struct Gates {
     }
 };
 
-// Tokens at T or beyond neither decay nor write (log w = 0, beta = 0).  Warp 0 does it, two
-// tokens a lane: the loads (fetch) ahead of the rest; the caller's barrier publishes it.
+// Tokens at T or beyond neither decay nor write (log w = 0, beta = 0).  One warp does it (the first,
+// or that whose threads pass 0 .. 31 as tid), two tokens a lane: the loads (fetch) ahead of the
+// rest; the caller's barrier publishes it.
 template <typename IO>
 struct RawGates {
     IO omega[2], beta[2];
 };
 template <typename IO>
 __device__ __forceinline__ RawGates<IO> fetch_gates(const IO* omega, const IO* beta, size_t base, int stride,
-                                                    int t0, int T) {
+                                                    int t0, int T, int tid = threadIdx.x) {
     RawGates<IO> r{};
-    if (threadIdx.x < 32)
+    if (tid < 32)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int t = 2 * threadIdx.x + i;
+            const int t = 2 * tid + i;
             if (t0 + t < T) {
                 r.omega[i] = omega[base + (size_t)(t0 + t) * stride];
                 r.beta[i] = beta[base + (size_t)(t0 + t) * stride];
@@ -70,9 +71,9 @@ __device__ __forceinline__ RawGates<IO> fetch_gates(const IO* omega, const IO* b
     return r;
 }
 template <typename IO>
-__device__ __forceinline__ void put_gates(Gates& s, const RawGates<IO>& raw, int t0, int T) {
-    if (threadIdx.x >= 32) return;
-    const int lane = threadIdx.x;
+__device__ __forceinline__ void put_gates(Gates& s, const RawGates<IO>& raw, int t0, int T, int tid = threadIdx.x) {
+    if (tid >= 32) return;
+    const int lane = tid;
     double l[2], run = 0.0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
