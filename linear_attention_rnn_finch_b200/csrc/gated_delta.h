@@ -30,9 +30,9 @@ struct GdrSegments {
     int count, blocks;
 };
 GdrSegments gdr_segments(int B, int T, int H, int ctas, int maps, float full, float part);
-// a, m: [head][last][64][64] fp32.  m[i] += a[i] m[i - 1] upwards, or m[i] += a[i + 1]^T m[i + 1]
-// downwards, 0 <= i < last.
-cudaError_t launch_gdr_join(const float* a, float* m, int heads, int last, bool back, cudaStream_t st);
+// at, a, s, d: [head][last][64][64] fp32, at[i] = a[i]^T.  s[i] += a[i] s[i - 1] upwards and, unless
+// a and d are null, d[i] += a[i + 1]^T d[i + 1] downwards, 0 <= i < last.
+cudaError_t launch_gdr_join(const float* at, const float* a, float* s, float* d, int heads, int last, cudaStream_t st);
 
 // Chunked on tensor cores, bf16 I/O.  s_out may equal s_in or be null; s_in null: zero.  ws: at
 // least gdr_chunked_bytes(B, T, H) bytes.

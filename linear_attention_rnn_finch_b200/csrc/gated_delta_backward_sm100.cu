@@ -37,10 +37,10 @@ struct Args {
     const float* s_in;
     uint8_t* ws;     // [head][block][S, E, G, dF]: hi, then lo part of each
     int blocks;
-    // segments of the sequence (gated_delta_segments.cu): A, then the states and the gradients at
+    // segments of the sequence (gated_delta_segments.cu): A^T, A, then the states and the gradients at
     // the borders, each [head][count - 1][64][64] fp32
     GdrSegments seg;
-    float *a, *s, *d;
+    float *at, *a, *s, *d;
     long long budget;   // cycles a wait of the second launch may take
 };
 
@@ -79,7 +79,7 @@ struct ChainSmem {
 // and do with two, but for A, which carries the state's fp32 gradient too.
 template <bool kBack, bool kStore, bool kExact>
 __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh, int seg, bool unit, const float* from,
-                                      float* to) {
+                                      float* to, float* to_t = nullptr) {
     const int H = p.in.H, HK = p.in.HK, b = bh / H, h = bh - b * H, hk = h / (H / HK);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int first = seg * p.seg.blocks, T = p.in.T - first * C, blocks = min(p.seg.blocks, p.blocks - first);
@@ -218,6 +218,7 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh, int s
         __syncthreads();
     }
     if (to) store_state(to, S, warp, lane);
+    if (unit) store_state_t(to_t, S, warp, lane);
 }
 
 // The chains of a head's segments, the longer ones (backward) first.
@@ -256,7 +257,7 @@ gated_delta_bwd_maps_kernel(const __grid_constant__ Args p) {
                             p.s + (border + seg) * C * C);
     } else {
         const int seg = i - 2 * last + 1;
-        chain<false, false, true>(s, p, bh, seg, true, nullptr, p.a + (border + seg) * C * C);
+        chain<false, false, true>(s, p, bh, seg, true, nullptr, p.a + (border + seg) * C * C, p.at + (border + seg) * C * C);
     }
 }
 
@@ -267,7 +268,8 @@ gated_delta_bwd_maps_kernel(const __grid_constant__ Args p) {
 // dP and dM, as two bf16 parts, over S and G's place.  Warp (w, half) reads tokens
 // 16 w .. 16 w + 15 and 32 columns of each result, in mma accumulator layout.  256 TMEM columns,
 // 94 KB and 128 registers: two CTAs an SM, of which one loads while the other computes.  (The same
-// on mma.sync: operand loads kept the shared-memory pipe 60 % busy, 749 us at B8 T4096 H32.)
+// on mma.sync: operand loads kept the shared-memory pipe 60 % busy, at B8 T4096 H32 749 us against
+// 530.)
 constexpr int kOutThreads = 256;
 constexpr uint32_t kTmemCols = 256;
 constexpr long long kDrain = 2000000000LL;   // cycles the last wait may take: about a second
@@ -672,28 +674,28 @@ cudaError_t run(Kernel kernel, unsigned grid, int threads, size_t smem, const Ar
 
 }  // namespace
 
-static GdrSegments segments(int B, int T, int H) { return gdr_segments(B, T, H, 2, 3, 2.5f, 2.0f); }
+static GdrSegments segments(int B, int T, int H) { return gdr_segments(B, T, H, 2, 3, 3.2f, 2.8f); }
 
 size_t gdr_backward_tc_bytes(int B, int T, int H) {
     const size_t heads = (size_t)B * H;
     return heads * ((T + C - 1) / C) * kBlockBytes +
-           3 * sizeof(float) * heads * (segments(B, T, H).count - 1) * C * C;
+           4 * sizeof(float) * heads * (segments(B, T, H).count - 1) * C * C;
 }
 
 cudaError_t launch_gdr_backward_tc(const GdrIn& in, const float* s_in, const GdrGrads& g, void* ws, long long budget,
                                    cudaStream_t st) {
     Args a{in, g, s_in, static_cast<uint8_t*>(ws), (in.T + C - 1) / C, segments(in.B, in.T, in.H),
-           nullptr, nullptr, nullptr, budget};
+           nullptr, nullptr, nullptr, nullptr, budget};
     const unsigned heads = (unsigned)(in.B * in.H), last = a.seg.count - 1;
     const size_t smem = sizeof(ChainSmem) + 1024;
     cudaError_t e;
     if (last > 0) {
-        a.a = reinterpret_cast<float*>(a.ws + (size_t)heads * a.blocks * kBlockBytes);
+        a.at = reinterpret_cast<float*>(a.ws + (size_t)heads * a.blocks * kBlockBytes);
+        a.a = a.at + (size_t)heads * last * C * C;
         a.s = a.a + (size_t)heads * last * C * C;
         a.d = a.s + (size_t)heads * last * C * C;
         e = run(gated_delta_bwd_maps_kernel, heads * (3 * last - 1), kTcThreads, smem, a, st);
-        if (e == cudaSuccess) e = launch_gdr_join(a.a, a.s, (int)heads, (int)last, false, st);
-        if (e == cudaSuccess) e = launch_gdr_join(a.a, a.d, (int)heads, (int)last, true, st);
+        if (e == cudaSuccess) e = launch_gdr_join(a.at, a.a, a.s, a.d, (int)heads, (int)last, st);
         if (e != cudaSuccess) return e;
     }
     e = run(gated_delta_bwd_chains_kernel, 2u * heads * a.seg.count, kTcThreads, smem, a, st);

@@ -19,7 +19,7 @@ constexpr int kStages = 3;   // a block in the chain, one in preparation, one on
 // Segments of the sequence (gated_delta_segments.cu); count 1: none.
 struct Segments {
     int count, blocks;
-    float* a;            // [head][count - 1][64][64]: A (its first place: the given state, which the
+    float* a;            // [head][count - 1][64][64]: A^T (its first place: the given state, which the
                          // call's last CTA may already be writing over when the first reads it)
     float* s;            // the same: B, then the state entering segment i + 1
 };
@@ -42,7 +42,7 @@ struct Args {
 };
 
 // One CTA's blocks: those of segment `seg` of head bh.  kOut: with outputs; otherwise only the
-// state is left, and `unit` leaves A instead of B.
+// state is left, and `unit` leaves A^T instead of B.
 template <bool kOut>
 __device__ __forceinline__ void walk(const Args& p, int bh, int seg, bool unit, const float* s_in, float* s_out) {
     extern __shared__ __align__(16) uint8_t raw[];
@@ -170,7 +170,7 @@ __device__ __forceinline__ void walk(const Args& p, int bh, int seg, bool unit, 
         }
         __syncthreads();
     }
-    if (s_out) store_state(s_out, S, warp, lane);
+    if (s_out) unit ? store_state_t(s_out, S, warp, lane) : store_state(s_out, S, warp, lane);
 }
 
 __global__ void __launch_bounds__(kTcThreads, 2)
@@ -194,7 +194,7 @@ gated_delta_maps_kernel(const __grid_constant__ Args p) {
 }
 
 Segments segments(int B, int T, int H) {
-    const GdrSegments g = gdr_segments(B, T, H, 1, 2, 2.3f, 1.7f);
+    const GdrSegments g = gdr_segments(B, T, H, 1, 2, 2.7f, 2.0f);
     return Segments{g.count, g.blocks, nullptr, nullptr};
 }
 
@@ -221,7 +221,7 @@ cudaError_t launch_gdr_chunked(const GdrIn& in, const float* s_in, float* s_out,
         a.seg.s = a.seg.a + (size_t)heads * last * C * C;
         cudaError_t e = run(gated_delta_maps_kernel, heads * (2 * last - 1), a, st);
         if (e != cudaSuccess) return e;
-        e = launch_gdr_join(a.seg.a, a.seg.s, (int)heads, (int)last, false, st);
+        e = launch_gdr_join(a.seg.a, nullptr, a.seg.s, nullptr, (int)heads, (int)last, st);
         if (e != cudaSuccess) return e;
     }
     return run(gated_delta_chunked_kernel, heads * a.seg.count, a, st);

@@ -276,6 +276,16 @@ __device__ __forceinline__ void store_state(float* dst, const float (&S)[8][4], 
         for (int e = 0; e < 4; ++e) dst[(8 * i + c + (e & 1)) * C + 16 * cw + r + 8 * (e >> 1)] = S[i][e];
 }
 
+// The same, [value][key].
+__device__ __forceinline__ void store_state_t(float* dst, const float (&S)[8][4], int cw, int lane) {
+    const int r = lane >> 2, c = 2 * (lane & 3);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float2*>(dst + (16 * cw + r + 8 * h) * C + 8 * i + c) = make_float2(S[i][2 * h], S[i][2 * h + 1]);
+}
+
 // S^T = factor S^T + X^T K: X^T as accumulators, taken in three parts (kExact) or two; kt: addr_bt of
 // K's 16 rows at chunk 0.
 template <bool kExact>
