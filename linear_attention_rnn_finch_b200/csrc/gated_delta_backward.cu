@@ -569,6 +569,9 @@ gated_delta_bwd_narrow_chains_kernel(Args p) {
 }
 
 // ---- 3: dQ, dK, dbeta, domega
+// Where key heads and chunks do not fill the device, each value head of a shared key head has a CTA
+// of its own (`apart`), which leaves its dQ and dK over T and E, and one more launch adds them up:
+// B2 T333 H4 over 2 key heads 32 + 6 us instead of 59.
 struct OutSmem {
     float q[kTileFloats], k[kTileFloats], dy[kTileFloats], e[kTileFloats], df[kTileFloats];
     float s[kTileFloats], g[kTileFloats], dp[kTileFloats], dm[kTileFloats], w[kTileFloats];
@@ -579,11 +582,12 @@ struct OutSmem {
 };
 
 __global__ void __launch_bounds__(kThreads)
-gated_delta_bwd_out_kernel(Args p) {
+gated_delta_bwd_out_kernel(Args p, bool apart) {
     extern __shared__ __align__(16) uint8_t raw[];
     OutSmem& s = *reinterpret_cast<OutSmem*>(raw);
-    const int n = blockIdx.x % p.NC, bk = blockIdx.x / p.NC;
-    const int H = p.in.H, HK = p.in.HK, T = p.in.T, b = bk / HK, hk = bk - b * HK, per = H / HK;
+    const int H = p.in.H, HK = p.in.HK, T = p.in.T, per = H / HK;
+    const int n = blockIdx.x % p.NC, i0 = blockIdx.x / p.NC, b = i0 / (apart ? H : HK), j0 = i0 - b * (apart ? H : HK);
+    const int h0 = apart ? j0 : j0 * per, h1 = apart ? h0 + 1 : h0 + per, hk = h0 / per;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ty = tid >> 4, tx = tid & 15;
     const int t0 = n * C;
     load_tokens(s.q, (const float*)p.in.q + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, t0, T);
@@ -591,7 +595,7 @@ gated_delta_bwd_out_kernel(Args p) {
     float dq[4][4], dk[4][4];
     clear(dq);
     clear(dk);
-    for (int h = hk * per; h < (hk + 1) * per; ++h) {
+    for (int h = h0; h < h1; ++h) {
         const size_t at = ((size_t)(b * H + h) * p.NC + n) * kMat;
         load_tokens(s.dy, (const float*)p.dy + ((size_t)b * T * H + h) * C, (size_t)H * C, t0, T);
         load_matrix(s.e, p.wE + at);
@@ -743,6 +747,17 @@ gated_delta_bwd_out_kernel(Args p) {
         }
         __syncthreads();
     }
+    if (apart) {
+        const size_t at = ((size_t)(b * H + h0) * p.NC + n) * kMat;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                p.wT[at + (4 * ty + i) * C + col<true>(tx, j)] = dq[i][j];
+                p.wE[at + (4 * ty + i) * C + col<true>(tx, j)] = dk[i][j];
+            }
+        return;
+    }
     float* oq = (float*)p.dq + ((size_t)b * T * HK + hk) * C;
     float* ok = (float*)p.dk + ((size_t)b * T * HK + hk) * C;
 #pragma unroll
@@ -757,11 +772,35 @@ gated_delta_bwd_out_kernel(Args p) {
     }
 }
 
-template <typename Kernel>
-cudaError_t run(Kernel kernel, unsigned grid, int threads, size_t smem, const Args& a, cudaStream_t st) {
+__global__ void __launch_bounds__(kThreads)
+gated_delta_bwd_heads_kernel(Args p) {   // four values a thread, four CTAs a chunk
+    const int H = p.in.H, HK = p.in.HK, T = p.in.T, per = H / HK, i = 4 * ((blockIdx.x & 3) * kThreads + threadIdx.x);
+    const int i0 = blockIdx.x >> 2, n = i0 % p.NC, bk = i0 / p.NC, b = bk / HK, hk = bk - b * HK, t = n * C + (i >> 6);
+    if (t >= T) return;
+    const size_t first = ((size_t)(b * H + hk * per) * p.NC + n) * kMat + i, step = (size_t)p.NC * kMat;
+    float q[4] = {0.f, 0.f, 0.f, 0.f}, k[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int h = 0; h < per; ++h) {
+        float x[4], y[4];
+        load_cols<4>(x, p.wT + first + h * step);
+        load_cols<4>(y, p.wE + first + h * step);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            q[e] += x[e];
+            k[e] += y[e];
+        }
+    }
+    const size_t o = (((size_t)b * T + t) * HK + hk) * C + (i & 63);
+    store_cols<4>((float*)p.dq + o, q);
+    store_cols<4>((float*)p.dk + o, k);
+}
+
+template <typename... More>
+cudaError_t run(void (*kernel)(Args, More...), unsigned grid, int threads, size_t smem, const Args& a, cudaStream_t st,
+                More... more) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, threads, smem, st>>>(a);
+    kernel<<<grid, threads, smem, st>>>(a, more...);
     return cudaGetLastError();
 }
 
@@ -788,7 +827,11 @@ cudaError_t launch_gdr_backward_f32(const GdrIn& in, const float* s_in, const Gd
     else
         e = run(gated_delta_bwd_chains_f32_kernel, 2 * heads, kChainThreads, sizeof(ChainSmem), a, st);
     if (e != cudaSuccess) return e;
-    return run(gated_delta_bwd_out_kernel, (unsigned)(in.B * in.HK) * (unsigned)NC, kThreads, sizeof(OutSmem), a, st);
+    const unsigned groups = (unsigned)(in.B * in.HK) * (unsigned)NC;
+    const bool apart = in.H > in.HK && groups < (unsigned)kSms;
+    e = run(gated_delta_bwd_out_kernel, apart ? heads * NC : groups, kThreads, sizeof(OutSmem), a, st, apart);
+    if (e != cudaSuccess || !apart) return e;
+    return run(gated_delta_bwd_heads_kernel, 4 * groups, kThreads, 0, a, st);
 }
 
 }  // namespace goldwkv
