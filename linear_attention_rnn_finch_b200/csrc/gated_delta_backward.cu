@@ -23,8 +23,10 @@
 // The fp32 path, where the CUDA cores bound it.  Three launches: what depends on no state,
 // parallel over chunks (T, P^T dY, scale (g Q)^T dY); the states S forward and the gradients G
 // backward, chains over a head's chunks of three 64 x 64 x 64 products each that need nothing
-// of each other, in CTAs of their own; and dQ, dK, db, domega, parallel over chunks, a CTA per
-// key head that adds up its value heads in registers (no atomics: the same bits every time).
+// of each other, in CTAs of their own; and dQ, dK, db, domega, parallel over chunks.  There a CTA
+// has a key head and adds up its value heads in registers; where that would leave SMs without
+// one, it has a value head, and a fourth launch adds up dQ and dK of those that share a key head,
+// in their order.  No atomics: the same bits every time.
 // All products are fp32 FMAs over shared-memory tiles.
 #include "common.cuh"
 #include "gated_delta.h"

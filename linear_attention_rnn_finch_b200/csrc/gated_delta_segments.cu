@@ -21,8 +21,8 @@ constexpr int kSms = 148;
 // parts.  A CTA takes 4 value columns of a head (they are independent).  Lanes are rows, a warp
 // contracts 16 of the 64 k for 32 of them: its 16 values of A (of A^T forward, so that lanes read
 // adjacent ones) come straight into registers, two borders ahead, and the matrix multiplied is
-// read from shared memory by all lanes alike.  The four warps of a row are added up in shared memory.  0.58 us a border (with A
-// in shared memory too, four results a thread, 1.9).
+// read from shared memory by all lanes alike.  The four warps of a row are added up in shared
+// memory.  0.58 us a border (with A in shared memory too, four results a thread, 1.9).
 constexpr int kThreads = 256, kCols = 4;
 template <bool kBack>
 __device__ __forceinline__ void join(const float* __restrict__ a, float* m, int last, int cta) {
