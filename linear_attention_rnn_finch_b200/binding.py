@@ -9,6 +9,7 @@ was not built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 from pathlib import Path
 
 import torch
@@ -687,6 +688,18 @@ def _workspace(workspace, need, device):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+def _on_its_stream(fn):
+    """Outputs and workspaces of a call with `stream` are allocated on that stream: one that is
+    freed before the stream has come to the call is given to later work of the same stream only."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, stream=stream, **kw)
+    return call
+
+
 def _gdr_args(q, k, v, omega, beta, lead):
     """Checks of q, k [*lead, HK, D], v [*lead, H, D], omega, beta [*lead, H]; (H, HK, D) and the
     five addresses."""
@@ -712,6 +725,7 @@ def gated_delta_backward_workspace_bytes(B, T, H, HK, D, io_dtype) -> int:
     return int(load().gated_delta_backward_workspace_bytes(B, T, H, HK, D, _io(io_dtype)))
 
 
+@_on_its_stream
 def gated_delta_prefill(q, k, v, omega, beta, state_in=None, *, scale=1.0, y=None, state_out=None,
                         want_state=True, workspace=None, stream=None):
     """The gated delta rule over T tokens (include/goldwkv.h, gated_delta_prefill): q, k
@@ -739,6 +753,7 @@ def gated_delta_prefill(q, k, v, omega, beta, state_in=None, *, scale=1.0, y=Non
     return y, state_out
 
 
+@_on_its_stream
 def gated_delta_decode_step(q, k, v, omega, beta, state, *, scale=1.0, y=None, stream=None):
     """One token of the gated delta rule: q, k [B, HK, D], v [B, H, D], omega, beta [B, H];
     ``state`` [B, H, D, D] fp32 is updated in place.  Returns y [B, H, D]."""
@@ -753,6 +768,7 @@ def gated_delta_decode_step(q, k, v, omega, beta, state, *, scale=1.0, y=None, s
     return y
 
 
+@_on_its_stream
 def gated_delta_backward(q, k, v, omega, beta, state_in, dy, dstate_out=None, *, scale=1.0,
                          want_dstate_in=True, workspace=None, stream=None):
     """Gradients of gated_delta_prefill given dy [B, T, H, D] (dtype of q) and the final
@@ -800,6 +816,7 @@ def _gn_args(x, gamma, beta, groups, act, gate):
                              _optional("gate", gate, dev, dt, shape))
 
 
+@_on_its_stream
 def group_norm_act(x, gamma, beta, eps=1e-5, *, groups, act="silu", gate=None, y=None,
                    workspace=None, stream=None):
     """Group norm over channels-last x [N, ..., C] (fp32 or bf16) with an activation
@@ -819,6 +836,7 @@ def group_norm_act(x, gamma, beta, eps=1e-5, *, groups, act="silu", gate=None, y
     return y
 
 
+@_on_its_stream
 def group_norm_act_backward(x, gamma, beta, eps, dy, *, groups, act="silu", gate=None,
                             workspace=None, stream=None):
     """Gradients of group_norm_act for dy (like x): (dx, dgamma [C] fp32, dbeta [C] fp32, dgate

@@ -5,8 +5,8 @@
 // Backward, with dz = dy act'(z) (or dy act(gate), and then dgate = dy z act'(gate)):
 //     dbeta = sum dz,   dgamma = sum dz h   (over n and positions),
 //     dh = dz gamma,    dx = (dh - mean(dh) - h mean(dh h)) / sqrt(var + eps).
-// Every pass is bound by memory; sums are fp32, of differences from a value of the data, so
-// that a mean far from zero costs no digits.
+// Every pass is bound by memory; sums are fp32, the squares' of differences from the mean (over
+// positions from a value of the data), so that a mean far from zero costs the variance no digits.
 //
 // One position (L = 1, each token's heads): a group is a contiguous run of `per` values held
 // in the registers of a few adjacent lanes, read once and written once in one launch.  A set of
