@@ -29,6 +29,7 @@
 // in their order.  No atomics: the same bits every time.
 // All products are fp32 FMAs over shared-memory tiles.
 #include "common.cuh"
+#include "dependent_launch.cuh"
 #include "gated_delta.h"
 #include "gated_delta_math.cuh"
 #include "warp_mma.cuh"
@@ -457,6 +458,7 @@ __global__ void __launch_bounds__(kChainThreads)
 gated_delta_bwd_chains_f32_kernel(Args p) {
     extern __shared__ __align__(16) uint8_t raw[];
     ChainSmem& s = *reinterpret_cast<ChainSmem*>(raw);
+    previous_ended();
     if (blockIdx.x & 1) chain<false>(s, p, blockIdx.x >> 1);
     else chain<true>(s, p, blockIdx.x >> 1);
 }
@@ -564,6 +566,7 @@ __device__ __forceinline__ void narrow_chain(NarrowSmem& sm, const Args& p, int 
 __global__ void __launch_bounds__(kNarrowThreads)
 gated_delta_bwd_narrow_chains_kernel(Args p) {
     __shared__ __align__(16) NarrowSmem s;
+    previous_ended();
     constexpr int kParts = C / kNarrow;
     const int i = blockIdx.x >> 1, bh = i / kParts, cols = kNarrow * (i - bh * kParts);
     if (blockIdx.x & 1) narrow_chain<false>(s, p, bh, cols);
@@ -594,6 +597,7 @@ gated_delta_bwd_out_kernel(Args p, bool apart) {
     const int t0 = n * C;
     load_tokens(s.q, (const float*)p.in.q + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, t0, T);
     load_tokens(s.k, (const float*)p.in.k + ((size_t)b * T * HK + hk) * C, (size_t)HK * C, t0, T);
+    previous_ended();
     float dq[4][4], dk[4][4];
     clear(dq);
     clear(dk);
@@ -778,6 +782,7 @@ __global__ void __launch_bounds__(kThreads)
 gated_delta_bwd_heads_kernel(Args p) {   // four values a thread, four CTAs a chunk
     const int H = p.in.H, HK = p.in.HK, T = p.in.T, per = H / HK, i = 4 * ((blockIdx.x & 3) * kThreads + threadIdx.x);
     const int i0 = blockIdx.x >> 2, n = i0 % p.NC, bk = i0 / p.NC, b = bk / HK, hk = bk - b * HK, t = n * C + (i >> 6);
+    previous_ended();
     if (t >= T) return;
     const size_t first = ((size_t)(b * H + hk * per) * p.NC + n) * kMat + i, step = (size_t)p.NC * kMat;
     float q[4] = {0.f, 0.f, 0.f, 0.f}, k[4] = {0.f, 0.f, 0.f, 0.f};
@@ -797,11 +802,12 @@ gated_delta_bwd_heads_kernel(Args p) {   // four values a thread, four CTAs a ch
     store_cols<4>((float*)p.dk + o, k);
 }
 
-template <typename... More>
-cudaError_t run(void (*kernel)(Args, More...), unsigned grid, int threads, size_t smem, const Args& a, cudaStream_t st,
+template <typename Kernel, typename... More>
+cudaError_t run(bool first, Kernel kernel, unsigned grid, int threads, size_t smem, const Args& a, cudaStream_t st,
                 More... more) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
+    if (!first) return launch_next(kernel, grid, threads, smem, st, a, more...);
     kernel<<<grid, threads, smem, st>>>(a, more...);
     return cudaGetLastError();
 }
@@ -822,18 +828,18 @@ cudaError_t launch_gdr_backward_f32(const GdrIn& in, const float* s_in, const Gd
     const Args a{in, g.dy, s_in, g.ds_out, g.ds_in, g.dq, g.dk, g.dv, g.domega, g.dbeta,
                  w, w + each, w + 2 * each, w + 3 * each, w + 4 * each, NC};
     const unsigned heads = (unsigned)(in.B * in.H);
-    cudaError_t e = run(gated_delta_bwd_local_kernel, 2 * heads * NC, kThreads, sizeof(LocalSmem), a, st);
+    cudaError_t e = run(true, gated_delta_bwd_local_kernel, 2 * heads * NC, kThreads, sizeof(LocalSmem), a, st);
     if (e != cudaSuccess) return e;
     if (2 * heads * (C / kNarrow) <= (unsigned)kSms)
-        e = run(gated_delta_bwd_narrow_chains_kernel, 2 * heads * (C / kNarrow), kNarrowThreads, 0, a, st);
+        e = run(false, gated_delta_bwd_narrow_chains_kernel, 2 * heads * (C / kNarrow), kNarrowThreads, 0, a, st);
     else
-        e = run(gated_delta_bwd_chains_f32_kernel, 2 * heads, kChainThreads, sizeof(ChainSmem), a, st);
+        e = run(false, gated_delta_bwd_chains_f32_kernel, 2 * heads, kChainThreads, sizeof(ChainSmem), a, st);
     if (e != cudaSuccess) return e;
     const unsigned groups = (unsigned)(in.B * in.HK) * (unsigned)NC;
     const bool apart = in.H > in.HK && groups < (unsigned)kSms;
-    e = run(gated_delta_bwd_out_kernel, apart ? heads * NC : groups, kThreads, sizeof(OutSmem), a, st, apart);
+    e = run(false, gated_delta_bwd_out_kernel, apart ? heads * NC : groups, kThreads, sizeof(OutSmem), a, st, apart);
     if (e != cudaSuccess || !apart) return e;
-    return run(gated_delta_bwd_heads_kernel, 4 * groups, kThreads, 0, a, st);
+    return run(false, gated_delta_bwd_heads_kernel, 4 * groups, kThreads, 0, a, st);
 }
 
 }  // namespace goldwkv

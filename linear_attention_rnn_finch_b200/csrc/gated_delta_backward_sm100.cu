@@ -16,6 +16,7 @@
 // products take anyway), transposed ([value][key] and [value][token], as the chains hold them)
 // and in the 128-byte-swizzled layout of a tcgen05.mma operand.  64 KB a head and block.
 #include "common.cuh"
+#include "dependent_launch.cuh"
 #include "gated_delta.h"
 #include "gated_delta_tiles.cuh"
 
@@ -226,6 +227,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 gated_delta_bwd_chains_kernel(const __grid_constant__ Args p) {
     extern __shared__ __align__(16) uint8_t raw[];
     ChainSmem& s = tiles::smem_aligned<ChainSmem>(raw);
+    previous_ended();
     const int n = p.seg.count, last = n - 1, half = (int)(gridDim.x >> 1);
     const bool back = (int)blockIdx.x < half;
     const int i = back ? blockIdx.x : blockIdx.x - half, bh = i / n, seg = i - bh * n;
@@ -340,6 +342,7 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
     if (warp == 0) ptx::tmem_alloc(&s.tmem, kTmemCols);
     copy_block<kOutThreads>(sq, (const bf16*)p.in.q + ko, (size_t)HK * C, t0, T, tid);
     copy_block<kOutThreads>(sk, (const bf16*)p.in.k + ko, (size_t)HK * C, t0, T, tid);
+    previous_ended();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -665,9 +668,10 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
 }
 
 template <typename Kernel>
-cudaError_t run(Kernel kernel, unsigned grid, int threads, size_t smem, const Args& a, cudaStream_t st) {
+cudaError_t run(bool first, Kernel kernel, unsigned grid, int threads, size_t smem, const Args& a, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
+    if (!first) return launch_next(kernel, grid, threads, smem, st, a);
     kernel<<<grid, threads, smem, st>>>(a);
     return cudaGetLastError();
 }
@@ -694,13 +698,13 @@ cudaError_t launch_gdr_backward_tc(const GdrIn& in, const float* s_in, const Gdr
         a.a = a.at + (size_t)heads * last * C * C;
         a.s = a.a + (size_t)heads * last * C * C;
         a.d = a.s + (size_t)heads * last * C * C;
-        e = run(gated_delta_bwd_maps_kernel, heads * (3 * last - 1), kTcThreads, smem, a, st);
+        e = run(true, gated_delta_bwd_maps_kernel, heads * (3 * last - 1), kTcThreads, smem, a, st);
         if (e == cudaSuccess) e = launch_gdr_join(a.at, a.a, a.s, a.d, (int)heads, (int)last, st);
         if (e != cudaSuccess) return e;
     }
-    e = run(gated_delta_bwd_chains_kernel, 2u * heads * a.seg.count, kTcThreads, smem, a, st);
+    e = run(last == 0, gated_delta_bwd_chains_kernel, 2u * heads * a.seg.count, kTcThreads, smem, a, st);
     if (e != cudaSuccess) return e;
-    return run(gated_delta_bwd_out_tc_kernel, (unsigned)(in.B * in.HK) * (unsigned)a.blocks, kOutThreads,
+    return run(false, gated_delta_bwd_out_tc_kernel, (unsigned)(in.B * in.HK) * (unsigned)a.blocks, kOutThreads,
                sizeof(OutSmem) + 1024, a, st);
 }
 

@@ -4,6 +4,7 @@
 // B8 T4096 H32: 321 us for 540 MB that it has to move (82 us at the memory's rate), token by token
 // on CUDA cores 1771; B1 T65531 H64 over 16 key heads, in two segments: 2.39 ms.
 #include "common.cuh"
+#include "dependent_launch.cuh"
 #include "gated_delta.h"
 #include "gated_delta_tiles.cuh"
 
@@ -175,6 +176,7 @@ __device__ __forceinline__ void walk(const Args& p, int bh, int seg, bool unit, 
 
 __global__ void __launch_bounds__(kTcThreads, 2)
 gated_delta_chunked_kernel(const __grid_constant__ Args p) {
+    previous_ended();
     const int bh = blockIdx.x / p.seg.count, seg = blockIdx.x - bh * p.seg.count, last = p.seg.count - 1;
     const float* s_in = p.s_in ? p.s_in + (size_t)bh * C * C : nullptr;
     if (seg > 0) s_in = p.seg.s + ((size_t)bh * last + seg - 1) * C * C;
@@ -199,10 +201,11 @@ Segments segments(int B, int T, int H) {
 }
 
 template <typename Kernel>
-cudaError_t run(Kernel kernel, unsigned grid, const Args& a, cudaStream_t st) {
+cudaError_t run(bool first, Kernel kernel, unsigned grid, const Args& a, cudaStream_t st) {
     const size_t smem = sizeof(Smem) + 1024;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
+    if (!first) return launch_next(kernel, grid, kTcThreads, smem, st, a);
     kernel<<<grid, kTcThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
@@ -219,12 +222,12 @@ cudaError_t launch_gdr_chunked(const GdrIn& in, const float* s_in, float* s_out,
     if (last > 0) {
         a.seg.a = static_cast<float*>(ws);
         a.seg.s = a.seg.a + (size_t)heads * last * C * C;
-        cudaError_t e = run(gated_delta_maps_kernel, heads * (2 * last - 1), a, st);
+        cudaError_t e = run(true, gated_delta_maps_kernel, heads * (2 * last - 1), a, st);
         if (e != cudaSuccess) return e;
         e = launch_gdr_join(a.seg.a, nullptr, a.seg.s, nullptr, (int)heads, (int)last, st);
         if (e != cudaSuccess) return e;
     }
-    return run(gated_delta_chunked_kernel, heads * a.seg.count, a, st);
+    return run(last == 0, gated_delta_chunked_kernel, heads * a.seg.count, a, st);
 }
 
 }  // namespace goldwkv

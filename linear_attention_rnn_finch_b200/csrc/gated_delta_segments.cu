@@ -7,6 +7,7 @@
 // v = 0) and B' of the segments, without outputs; this file's kernel walks the segments'
 // borders; the next launch runs all segments at once from the states at their borders.
 #include "common.cuh"
+#include "dependent_launch.cuh"
 #include "gated_delta.h"
 
 namespace goldwkv {
@@ -78,8 +79,9 @@ __device__ __forceinline__ void join(const float* __restrict__ a, float* m, int 
 // The states, and behind them (where d is given) the gradients.
 __global__ void __launch_bounds__(kThreads)
 gated_delta_join_kernel(const float* __restrict__ at, const float* __restrict__ a, float* s, float* d, int last, int ctas) {
-    if ((int)blockIdx.x < ctas) join<false>(at, s, last, blockIdx.x);
-    else join<true>(a, d, last, blockIdx.x - ctas);
+    previous_ended();
+    if ((int)blockIdx.x < ctas) join<false>(behind(at), s, last, blockIdx.x);
+    else join<true>(behind(a), d, last, blockIdx.x - ctas);
 }
 
 }  // namespace
@@ -108,8 +110,7 @@ GdrSegments gdr_segments(int B, int T, int H, int ctas, int maps, float full, fl
 
 cudaError_t launch_gdr_join(const float* at, const float* a, float* s, float* d, int heads, int last, cudaStream_t st) {
     const int ctas = heads * (C / kCols);
-    gated_delta_join_kernel<<<(unsigned)(d ? 2 * ctas : ctas), kThreads, 0, st>>>(at, a, s, d, last, ctas);
-    return cudaGetLastError();
+    return launch_next(gated_delta_join_kernel, (unsigned)(d ? 2 * ctas : ctas), kThreads, 0, st, at, a, s, d, last, ctas);
 }
 
 }  // namespace goldwkv

@@ -21,6 +21,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "dependent_launch.cuh"
 #include "group_norm_act.h"
 
 namespace goldwkv {
@@ -604,7 +605,8 @@ constexpr int kParamWarps = 32;   // few rows a warp: the loads' latency is all 
 __global__ void __launch_bounds__(32 * kParamWarps)
 group_norm_param_kernel(const float* __restrict__ part, long rows, int C, float* __restrict__ dgamma,
                         float* __restrict__ dbeta) {
-    sum_params<kParamWarps>(part, rows, C, blockIdx.x, dgamma, dbeta);
+    previous_ended();
+    sum_params<kParamWarps>(behind(part), rows, C, blockIdx.x, dgamma, dbeta);
 }
 
 // ------------------------------------------------------------------ several positions
@@ -788,7 +790,8 @@ group_norm_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
                         const float2* __restrict__ part, IO* __restrict__ y, Tiling t) {
     __shared__ float2 stat[kThreads * V];
     const Place p = place(t);
-    join_stats(part, eps, t, p, stat);
+    previous_ended();
+    join_stats(behind(part), eps, t, p, stat);
     if (!p.in) return;
     float mean[V], r[V], be[V];
     load<V>(gamma + p.c0, r);
@@ -826,7 +829,8 @@ group_norm_bwd_sums_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
     __shared__ float2 red[kThreads * V];
     const Place p = place(t);
     float2* stat = red;
-    join_stats(part, eps, t, p, stat);
+    previous_ended();
+    join_stats(behind(part), eps, t, p, stat);
     if (p.split == 0 && p.tile % t.parts == 0)
         for (int g = threadIdx.x; g < p.g_count; g += kThreads) stats[p.n * t.groups + p.g_begin + g] = stat[g];
     float mean[V], r[V], ga[V], be[V], sg[V], sb[V];
@@ -902,8 +906,11 @@ group_norm_bwd_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gat
                             float* __restrict__ dgamma, float* __restrict__ dbeta, unsigned ctas,
                             Tiling t) {
     __shared__ float2 sum[kThreads * V];
+    previous_ended();
+    stats = behind(stats);
+    sums = behind(sums);
     if (blockIdx.x >= ctas) {
-        sum_params<kThreads / 32>(rows, t.N * t.splits, t.C, (int)(blockIdx.x - ctas), dgamma, dbeta);
+        sum_params<kThreads / 32>(behind(rows), t.N * t.splits, t.C, (int)(blockIdx.x - ctas), dgamma, dbeta);
         return;
     }
     const Place p = place(t);
@@ -1056,9 +1063,10 @@ cudaError_t positions_fwd(const GroupNorm& a, void* y, void* ws, const Tiling& t
     float2* part = static_cast<float2*>(ws);
     const IO* x = (const IO*)a.x;
     group_norm_stats_kernel<IO, V><<<tile_ctas(t), kThreads, 0, st>>>(x, part, t);
-    group_norm_apply_kernel<IO, V, kGate, kSilu><<<tile_ctas(t), kThreads, 0, st>>>(
-        x, (const IO*)a.gate, a.gamma, a.beta, a.eps, part, (IO*)y, t);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_next(group_norm_apply_kernel<IO, V, kGate, kSilu>, tile_ctas(t), kThreads, 0, st, x,
+                       (const IO*)a.gate, a.gamma, a.beta, a.eps, part, (IO*)y, t);
 }
 template <typename IO, int V, bool kGate, bool kSilu>
 cudaError_t positions_bwd(const GroupNorm& a, const void* dy, void* dx, float* dgamma, float* dbeta,
@@ -1071,11 +1079,13 @@ cudaError_t positions_bwd(const GroupNorm& a, const void* dy, void* dx, float* d
     const IO *x = (const IO*)a.x, *gate = (const IO*)a.gate, *d = (const IO*)dy;
     const unsigned grid = tile_ctas(t), params = (unsigned)((2 * t.C + 31) / 32);
     group_norm_stats_kernel<IO, V><<<grid, kThreads, 0, st>>>(x, part, t);
-    group_norm_bwd_sums_kernel<IO, V, kGate, kSilu><<<grid, kThreads, 0, st>>>(
-        x, gate, a.gamma, a.beta, a.eps, part, d, (IO*)dgate, stats, rows, sums, t);
-    group_norm_bwd_apply_kernel<IO, V, kGate, kSilu><<<grid + params, kThreads, 0, st>>>(
-        x, gate, a.gamma, a.beta, stats, sums, d, (IO*)dx, rows, dgamma, dbeta, grid, t);
-    return cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = launch_next(group_norm_bwd_sums_kernel<IO, V, kGate, kSilu>, grid, kThreads, 0, st, x, gate, a.gamma, a.beta,
+                    a.eps, part, d, (IO*)dgate, stats, rows, sums, t);
+    if (e != cudaSuccess) return e;
+    return launch_next(group_norm_bwd_apply_kernel<IO, V, kGate, kSilu>, grid + params, kThreads, 0, st, x, gate,
+                       a.gamma, a.beta, stats, sums, d, (IO*)dx, rows, dgamma, dbeta, grid, t);
 }
 // f(vector width, gate, silu), the three as compile-time constants
 template <typename F>
@@ -1155,9 +1165,8 @@ cudaError_t backward_io(const GroupNorm& a, const void* dy, void* dx, float* dga
               : u == 8 ? rows_bwd<IO, 1, 8>(a, dy, dx, dgate, part, s, st)
                        : rows_bwd<IO, 1, 0>(a, dy, dx, dgate, part, s, st);
         if (e != cudaSuccess) return e;
-        group_norm_param_kernel<<<(unsigned)((2 * a.C + 31) / 32), 32 * kParamWarps, 0, st>>>(part, s.streams, a.C,
-                                                                                    dgamma, dbeta);
-        return cudaGetLastError();
+        return launch_next(group_norm_param_kernel, (unsigned)((2 * a.C + 31) / 32), 32 * kParamWarps, 0, st, part,
+                           s.streams, a.C, dgamma, dbeta);
     }
     const Tiling t = tiling(a.N, a.L, a.C, a.groups);
     return with_constants(a, t, [&](auto v, auto gate, auto silu) {
