@@ -790,30 +790,56 @@ group_norm_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gate,
                         const float2* __restrict__ part, IO* __restrict__ y, Tiling t) {
     __shared__ float2 stat[kThreads * V];
     const Place p = place(t);
+    const size_t base = ((size_t)p.n * t.L) * t.C + p.c0;
+    // A turn of positions' loads is issued before the turn ahead of it is worked on; the first needs
+    // no statistics.  [8, 16384, 512] bf16 with a gate 138 -> 100 us, [2, 16384, 512] fp32 59 -> 48;
+    // eight positions a turn 104 and 67.
+    constexpr int kTurn = sizeof(IO) == 4 ? 2 : 4;
+    Raw<IO, V> rx[kTurn], rg[kTurn];
+    float mean[V], r[V], be[V];
+    auto fetch = [&](long l) {
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i, l += t.lanes)
+            if (l < p.l1) {
+                rx[i] = load_raw<IO, V>(x + base + (size_t)l * t.C);
+                if (kGate) rg[i] = load_raw<IO, V>(gate + base + (size_t)l * t.C);
+            }
+    };
+    if (p.in) {
+        load<V>(gamma + p.c0, r);
+        load<V>(beta + p.c0, be);
+        fetch(p.l0);
+    }
     previous_ended();
     join_stats(behind(part), eps, t, p, stat);
     if (!p.in) return;
-    float mean[V], r[V], be[V];
-    load<V>(gamma + p.c0, r);
-    load<V>(beta + p.c0, be);
     each_group<V>(t, p.c0, [&](int e, int g) {
         const float2 st = stat[g - p.g_begin];
         mean[e] = st.x;
         r[e] *= st.y;
     });
-    const size_t base = ((size_t)p.n * t.L) * t.C + p.c0;
-#pragma unroll 4
-    for (long l = p.l0; l < p.l1; l += t.lanes) {
-        const size_t o = base + (size_t)l * t.C;
-        float v[V], gt[V];
-        load<V>(x + o, v);
-        if (kGate) load<V>(gate + o, gt);
+    for (long l = p.l0; l < p.l1; l += kTurn * t.lanes) {
+        Raw<IO, V> cx[kTurn], cg[kTurn];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float z = fmaf(v[e] - mean[e], r[e], be[e]);
-            v[e] = kGate ? z * act<IO>(gt[e], kSilu) : act<IO>(z, kSilu);
+        for (int i = 0; i < kTurn; ++i) {
+            cx[i] = rx[i];
+            if (kGate) cg[i] = rg[i];
         }
-        store<V>(y + o, v);
+        fetch(l + kTurn * t.lanes);
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i) {
+            const long at = l + i * t.lanes;
+            if (at >= p.l1) break;
+            float v[V], gt[V];
+            convert(cx[i], v);
+            if (kGate) convert(cg[i], gt);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float z = fmaf(v[e] - mean[e], r[e], be[e]);
+                v[e] = kGate ? z * act<IO>(gt[e], kSilu) : act<IO>(z, kSilu);
+            }
+            store<V>(y + base + (size_t)at * t.C, v);
+        }
     }
 }
 
