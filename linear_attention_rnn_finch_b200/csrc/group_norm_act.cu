@@ -855,37 +855,65 @@ group_norm_bwd_sums_kernel(const IO* __restrict__ x, const IO* __restrict__ gate
     __shared__ float2 red[kThreads * V];
     const Place p = place(t);
     float2* stat = red;
+    const size_t base = ((size_t)p.n * t.L) * t.C + p.c0;
+    // as in group_norm_apply_kernel: [8, 16384, 512] bf16 with a gate 296 -> 212 us for this launch
+    // and the next, [2, 16384, 512] fp32 108 -> 90; with a position more a turn 241 and 123
+    constexpr int kTurn = sizeof(IO) == 4 ? 1 : 2;
+    Raw<IO, V> rx[kTurn], rd[kTurn], rg[kTurn];
+    float mean[V], r[V], ga[V], be[V], sg[V], sb[V];
+    auto fetch = [&](long l) {
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i, l += t.lanes)
+            if (l < p.l1) {
+                const size_t o = base + (size_t)l * t.C;
+                rx[i] = load_raw<IO, V>(x + o);
+                rd[i] = load_raw<IO, V>(dy + o);
+                if (kGate) rg[i] = load_raw<IO, V>(gate + o);
+            }
+    };
+    if (p.in) {
+        load<V>(gamma + p.c0, ga);
+        load<V>(beta + p.c0, be);
+        fetch(p.l0);
+    }
     previous_ended();
     join_stats(behind(part), eps, t, p, stat);
     if (p.split == 0 && p.tile % t.parts == 0)
         for (int g = threadIdx.x; g < p.g_count; g += kThreads) stats[p.n * t.groups + p.g_begin + g] = stat[g];
-    float mean[V], r[V], ga[V], be[V], sg[V], sb[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) sg[e] = sb[e] = 0.f;
     if (p.in) {
-        load<V>(gamma + p.c0, ga);
-        load<V>(beta + p.c0, be);
         each_group<V>(t, p.c0, [&](int e, int g) {
             const float2 st = stat[g - p.g_begin];
             mean[e] = st.x;
             r[e] = st.y;
         });
-        const size_t base = ((size_t)p.n * t.L) * t.C + p.c0;
-#pragma unroll 4
-        for (long l = p.l0; l < p.l1; l += t.lanes) {
-            const size_t o = base + (size_t)l * t.C;
-            float v[V], d[V], gt[V];
-            load<V>(x + o, v);
-            load<V>(dy + o, d);
-            if (kGate) load<V>(gate + o, gt);
+        for (long l = p.l0; l < p.l1; l += kTurn * t.lanes) {
+            Raw<IO, V> cx[kTurn], cd[kTurn], cg[kTurn];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float h = (v[e] - mean[e]) * r[e];
-                const float dz = value_grad<IO, kGate>(h, ga[e], be[e], d[e], gt[e], kSilu);
-                sg[e] = fmaf(dz, h, sg[e]);
-                sb[e] += dz;
+            for (int i = 0; i < kTurn; ++i) {
+                cx[i] = rx[i];
+                cd[i] = rd[i];
+                if (kGate) cg[i] = rg[i];
             }
-            if (kGate) store<V>(dgate + o, gt);
+            fetch(l + kTurn * t.lanes);
+#pragma unroll
+            for (int i = 0; i < kTurn; ++i) {
+                const long at = l + i * t.lanes;
+                if (at >= p.l1) break;
+                float v[V], d[V], gt[V];
+                convert(cx[i], v);
+                convert(cd[i], d);
+                if (kGate) convert(cg[i], gt);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float h = (v[e] - mean[e]) * r[e];
+                    const float dz = value_grad<IO, kGate>(h, ga[e], be[e], d[e], gt[e], kSilu);
+                    sg[e] = fmaf(dz, h, sg[e]);
+                    sb[e] += dz;
+                }
+                if (kGate) store<V>(dgate + base + (size_t)at * t.C, gt);
+            }
         }
     }
     __syncthreads();   // stat is read
@@ -932,14 +960,34 @@ group_norm_bwd_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gat
                             float* __restrict__ dgamma, float* __restrict__ dbeta, unsigned ctas,
                             Tiling t) {
     __shared__ float2 sum[kThreads * V];
-    previous_ended();
-    stats = behind(stats);
-    sums = behind(sums);
     if (blockIdx.x >= ctas) {
+        previous_ended();
         sum_params<kThreads / 32>(behind(rows), t.N * t.splits, t.C, (int)(blockIdx.x - ctas), dgamma, dbeta);
         return;
     }
     const Place p = place(t);
+    const size_t base = ((size_t)p.n * t.L) * t.C + p.c0;
+    constexpr int kTurn = sizeof(IO) == 4 ? 1 : 2;
+    Raw<IO, V> rx[kTurn], rd[kTurn], rg[kTurn];
+    float mean[V], r[V], ga[V], be[V], s1[V], s2[V];
+    auto fetch = [&](long l) {
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i, l += t.lanes)
+            if (l < p.l1) {
+                const size_t o = base + (size_t)l * t.C;
+                rx[i] = load_raw<IO, V>(x + o);
+                rd[i] = load_raw<IO, V>(dy + o);
+                if (kGate) rg[i] = load_raw<IO, V>(gate + o);
+            }
+    };
+    if (p.in) {
+        load<V>(gamma + p.c0, ga);
+        load<V>(beta + p.c0, be);
+        fetch(p.l0);
+    }
+    previous_ended();
+    stats = behind(stats);
+    sums = behind(sums);
     {
         const int lanes = group_lanes(p.g_count), lane = threadIdx.x & (lanes - 1), items = t.splits * t.parts;
         const float inv = 1.f / ((float)t.L * (float)t.per);
@@ -959,9 +1007,6 @@ group_norm_bwd_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gat
         __syncthreads();
     }
     if (!p.in) return;
-    float mean[V], r[V], ga[V], be[V], s1[V], s2[V];
-    load<V>(gamma + p.c0, ga);
-    load<V>(beta + p.c0, be);
     each_group<V>(t, p.c0, [&](int e, int g) {
         const float2 st = stats[p.n * t.groups + g], su = sum[g - p.g_begin];
         mean[e] = st.x;
@@ -969,22 +1014,32 @@ group_norm_bwd_apply_kernel(const IO* __restrict__ x, const IO* __restrict__ gat
         s1[e] = su.x;
         s2[e] = su.y;
     });
-    const size_t base = ((size_t)p.n * t.L) * t.C + p.c0;
-#pragma unroll 4
-    for (long l = p.l0; l < p.l1; l += t.lanes) {
-        const size_t o = base + (size_t)l * t.C;
-        float v[V], d[V], gt[V];
-        load<V>(x + o, v);
-        load<V>(dy + o, d);
-        if (kGate) load<V>(gate + o, gt);
+    for (long l = p.l0; l < p.l1; l += kTurn * t.lanes) {
+        Raw<IO, V> cx[kTurn], cd[kTurn], cg[kTurn];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float h = (v[e] - mean[e]) * r[e];
-            const float dz = d[e] * (kGate ? act<IO>(gt[e], kSilu)
-                                          : act_grad<IO>(fmaf(h, ga[e], be[e]), kSilu).y);
-            d[e] = r[e] * (dz * ga[e] - s1[e] - h * s2[e]);
+        for (int i = 0; i < kTurn; ++i) {
+            cx[i] = rx[i];
+            cd[i] = rd[i];
+            if (kGate) cg[i] = rg[i];
         }
-        store<V>(dx + o, d);
+        fetch(l + kTurn * t.lanes);
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i) {
+            const long at = l + i * t.lanes;
+            if (at >= p.l1) break;
+            float v[V], d[V], gt[V];
+            convert(cx[i], v);
+            convert(cd[i], d);
+            if (kGate) convert(cg[i], gt);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float h = (v[e] - mean[e]) * r[e];
+                const float dz = d[e] * (kGate ? act<IO>(gt[e], kSilu)
+                                              : act_grad<IO>(fmaf(h, ga[e], be[e]), kSilu).y);
+                d[e] = r[e] * (dz * ga[e] - s1[e] - h * s2[e]);
+            }
+            store<V>(dx + base + (size_t)at * t.C, d);
+        }
     }
 }
 
@@ -1044,7 +1099,7 @@ Tiling tiling(long N, long L, int C, int groups) {
     t.vecs = (t.width + t.V - 1) / t.V;
     t.lanes = kThreads / t.vecs;
     // splits: two CTAs an SM (each pays a few hundred instructions a thread to join its groups:
-    // [8, 4093, 320] 25 us, with three or four 27), but at least 4 positions a lane
+    // [8, 4093, 320] 17 us, with one 24, with three or four 23), but at least 4 positions a lane
     const long ctas = N * t.tiles;
     long want = (2L * kSms + ctas - 1) / ctas;
     const long limit = (L + 4L * t.lanes - 1) / (4L * t.lanes);
