@@ -150,19 +150,23 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh, int s
             float f[2][4], e[2][4];   // S^T K^T (or G^T K^T)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t hi[4], lo[4], kb[4];
+                uint32_t a0[4], a1[4], a2[4], kb[4];
                 ldsm4(kb, step(kt + ab, i));
-                split_a(hi, lo, S[2 * i], S[2 * i + 1]);
+                if (kExact) split_a3(a0, a1, a2, S[2 * i], S[2 * i + 1]);
+                else split_a(a0, a1, S[2 * i], S[2 * i + 1]);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {   // hi and lo parts in chains of their own
+                for (int u = 0; u < 2; ++u) {   // the first part and the smaller ones in sums of their own
                     if (i == 0) {
-                        mma0(f[u], hi, kb[2 * u], kb[2 * u + 1]);
-                        mma0(e[u], lo, kb[2 * u], kb[2 * u + 1]);
+                        mma0(f[u], a0, kb[2 * u], kb[2 * u + 1]);
+                        mma0(e[u], a1, kb[2 * u], kb[2 * u + 1]);
                     } else {
-                        mma(f[u], hi, kb[2 * u], kb[2 * u + 1]);
-                        mma(e[u], lo, kb[2 * u], kb[2 * u + 1]);
+                        mma(f[u], a0, kb[2 * u], kb[2 * u + 1]);
+                        mma(e[u], a1, kb[2 * u], kb[2 * u + 1]);
                     }
                 }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (kExact) mma(e[u], a2, kb[2 * u], kb[2 * u + 1]);
             }
             uint32_t xv[4];   // V^T or dY^T, as the A operand [value][token]
             ldsm4t(xv, sx + o + row * 128 + act);
@@ -212,8 +216,7 @@ __device__ __forceinline__ void chain(ChainSmem& s, const Args& p, int bh, int s
                     scale_cols(f[u], make_float2(p.in.scale * g[u].x, p.in.scale * g[u].y));
                     scale_cols(e[u], make_float2(-g[u].x, -g[u].y));
                 }
-                update_state<kExact>(S, pr.g_end[j], f, kt + abt + (sq - sk));
-                update_state<kExact>(S, 1.f, e, kt + abt);
+                update_state<kExact, true>(S, pr.g_end[j], e, kt + abt, f, kt + abt + (sq - sk));
             }
         }
         __syncthreads();

@@ -1,8 +1,8 @@
 // Chunked prefill of the gated delta rule, bf16 inputs, on tensor cores (sm_100a).  The algebra,
 // the division of labour and what bounds it are in gated_delta_tiles.cuh.
 //
-// B8 T4096 H32: 321 us for 540 MB that it has to move (82 us at the memory's rate), token by token
-// on CUDA cores 1771; B1 T65531 H64 over 16 key heads, in two segments: 2.39 ms.
+// B8 T4096 H32: 353 us for 540 MB that it has to move (82 us at the memory's rate), token by token
+// on CUDA cores 1771; B1 T65531 H64 over 16 key heads, in two segments: 2.69 ms.
 #include "common.cuh"
 #include "dependent_launch.cuh"
 #include "gated_delta.h"
@@ -109,30 +109,36 @@ __device__ __forceinline__ void walk(const Args& p, int bh, int seg, bool unit, 
         for (int j = 0; j < subs; ++j) {
             const int row = kSub * j;
             const uint32_t kt = sk + o + row * 128;
-            // S^T K^T and S^T Q^T
-            float f[2][4], y[2][4];
+            // S^T K^T, all three parts of S, and S^T Q^T; the smaller parts' terms in sums of their own
+            float f[2][4], e[2][4], y[2][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t hi[4], lo[4], kb[4], qb[4];
+                uint32_t a0[4], a1[4], a2[4], kb[4], qb[4];
                 ldsm4(kb, step(kt + ab, i));
                 if (kOut) ldsm4(qb, step(kt + ab, i) + (sq - sk));
-                split_a(hi, lo, S[2 * i], S[2 * i + 1]);
+                split_a3(a0, a1, a2, S[2 * i], S[2 * i + 1]);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     if (i == 0) {
-                        mma0(f[u], lo, kb[2 * u], kb[2 * u + 1]);
-                        if (kOut) mma0(y[u], lo, qb[2 * u], qb[2 * u + 1]);
+                        mma0(e[u], a2, kb[2 * u], kb[2 * u + 1]);
+                        mma0(f[u], a0, kb[2 * u], kb[2 * u + 1]);
+                        if (kOut) mma0(y[u], a1, qb[2 * u], qb[2 * u + 1]);
                     } else {
-                        mma(f[u], lo, kb[2 * u], kb[2 * u + 1]);
-                        if (kOut) mma(y[u], lo, qb[2 * u], qb[2 * u + 1]);
+                        mma(e[u], a2, kb[2 * u], kb[2 * u + 1]);
+                        mma(f[u], a0, kb[2 * u], kb[2 * u + 1]);
+                        if (kOut) mma(y[u], a1, qb[2 * u], qb[2 * u + 1]);
                     }
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    mma(f[u], hi, kb[2 * u], kb[2 * u + 1]);
-                    if (kOut) mma(y[u], hi, qb[2 * u], qb[2 * u + 1]);
+                    mma(e[u], a1, kb[2 * u], kb[2 * u + 1]);
+                    if (kOut) mma(y[u], a0, qb[2 * u], qb[2 * u + 1]);
                 }
             }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) f[u][x] += e[u][x];
             // F^T = V^T - g S^T K^T
             float2 g[2];
             uint32_t vv[4];
@@ -142,7 +148,6 @@ __device__ __forceinline__ void walk(const Args& p, int bh, int seg, bool unit, 
                 g[u] = *reinterpret_cast<const float2*>(&pr.g[row + 8 * u + c]);
                 value_minus(f[u], g[u], vv[2 * u], vv[2 * u + 1]);
             }
-            float e[2][4];
             times_t<true>(e, f, pt + j * kTile16, lane);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -151,7 +156,6 @@ __device__ __forceinline__ void walk(const Args& p, int bh, int seg, bool unit, 
                 for (int x = 0; x < 4; ++x) f[u][x] = e[u][x];
                 scale_cols(f[u], *reinterpret_cast<const float2*>(&pr.to_end[row + 8 * u + c]));
             }
-            update_state<true>(S, pr.g_end[j], f, kt + abt);
             if (kOut) {
                 // Y^T = scale g (S^T Q^T) + (b E)^T P^T
                 uint32_t p0[4], p1[4], hi[4], lo[4];
@@ -165,6 +169,9 @@ __device__ __forceinline__ void walk(const Args& p, int bh, int seg, bool unit, 
                     mma(y[u], hi, p1[2 * u], p1[2 * u + 1]);
                     mma(y[u], hi, p0[2 * u], p0[2 * u + 1]);
                 }
+            }
+            update_state<true>(S, pr.g_end[j], f, kt + abt);
+            if (kOut) {
                 const int tr = n * C + row;
                 store_tokens(yp + (size_t)tr * H * C, (size_t)H * C, T - tr, y, s.y[warp], lane);
             }

@@ -19,20 +19,27 @@
 // (the preparation) work one block ahead: they issue the copies of the block after it, and
 // form decays, T and P of one sub-chunk each.  The two halves meet once a block.
 //
-// Operands that are not the caller's bf16 values are kept as sums of bf16 parts: two (2^-17 of the
-// value) where they only lead to bf16 results, and for S as it meets K and Q; three (2^-25) for
-// what comes back in the fp32 state, T, F and the terms added to S, so that it is as exact as fp32
-// sums make it (with two parts of F and of those terms it is off by 3e-6 of its norm instead of
-// 2e-7; with two parts of T, and keys alike with strengths near two, by 1e-4 after 150 tokens).
-// The ten matrix instructions more in 64 take B8 T4096 H32 from 287 to 321 us.  Sums are fp32.
+// Operands that are not the caller's bf16 values are kept as sums of bf16 parts.  Three (2^-25 of
+// the value) for what comes back in the fp32 state: S against K, T, F and the terms added to S,
+// whose products are summed on their own and added to S by FMAs.  The state is then as exact as
+// fp32 sums make it: off by 1e-7 to 3e-7 of its norm for strengths up to one and any decay.  (Two
+// parts of S against K: 2e-6 where little is forgotten; of F and the terms: 3e-6; of T, with keys
+// alike and strengths near two: 1e-4 after 150 tokens.)  Strength two without decay forgets nothing
+// ever: 8e-6 after 4096 tokens, where fp32 token by token is off by 1.4e-6, since the tensor cores
+// cut sums off rather than rounding them (two parts of S against K: 3e-5).
+// Two parts (2^-17) where a value only leads to bf16 results: S against Q, P and b E in the readout.
+// Outputs then differ from those of fp32 sums by 1.3e-4 of their norm, single steps of bf16 where
+// a value lies at the edge of a rounding; their error against 64 bits is that of the rounding either
+// way, 1.7e-3.  Three parts there take B8 T4096 H32 a tenth longer.
+// B8 T4096 H32 takes 353 us so, with two parts against K 322, with two throughout 287.
 //
 // mma.sync, not tcgen05: the chain's products are 16 x 16 x 64 and smaller and each needs the one
 // before it, which as tcgen05.mma is a round through shared memory, a barrier, a commit and TMEM
 // loads (a group of 64 x 64 x 64 products takes 1000 cycles and more in the backward's second
 // launch), against 21 cycles for a register-to-register mma.sync, one every 8 a scheduler.  What
 // bounds a chain is its schedulers: an mma.sync keeps the FP32 pipe's dispatch for about 6 of its 8
-// cycles, so the 74 of a sub-chunk and the 400 instructions beside them hardly overlap (1250 cycles
-// a sub-chunk where the tensor pipe needs 600; a second CTA on the SM adds an eighth).
+// cycles, so the 82 of a sub-chunk and the 400 instructions beside them hardly overlap (1370 cycles
+// a sub-chunk where the tensor pipe needs 660; a second CTA on the SM adds an eighth).
 #pragma once
 
 #include "gated_delta.h"
@@ -286,27 +293,42 @@ __device__ __forceinline__ void store_state_t(float* dst, const float (&S)[8][4]
             *reinterpret_cast<float2*>(dst + (16 * cw + r + 8 * h) * C + 8 * i + c) = make_float2(S[i][2 * h], S[i][2 * h + 1]);
 }
 
-// S^T = factor S^T + X^T K: X^T as accumulators, taken in three parts (kExact) or two; kt: addr_bt of
-// K's 16 rows at chunk 0.
-template <bool kExact>
-__device__ __forceinline__ void update_state(float (&S)[8][4], float factor, const float (&x)[2][4], uint32_t kt) {
-    uint32_t a0[4], a1[4], a2[4];
-    if (kExact) split_a3(a0, a1, a2, x[0], x[1]);
-    else split_a(a0, a1, x[0], x[1]);
+// S^T = factor S^T + X^T K (+ Z^T Q with kTwo): X^T, Z^T as accumulators, taken in three parts
+// (kExact) or two; kt, qt: addr_bt of K's and Q's 16 rows at chunk 0.  The products are summed on
+// their own and added to S by FMAs, which round to nearest: an mma.sync cuts its sum off, so that
+// S as its accumulator lost a little of its size in every one of three.
+template <bool kExact, bool kTwo = false>
+__device__ __forceinline__ void update_state(float (&S)[8][4], float factor, const float (&x)[2][4], uint32_t kt,
+                                             const float (*z)[4] = nullptr, uint32_t qt = 0) {
+    uint32_t a[3][4], c[3][4];
+    if (kExact) split_a3(a[0], a[1], a[2], x[0], x[1]);
+    else split_a(a[0], a[1], x[0], x[1]);
+    if (kTwo) {
+        if (kExact) split_a3(c[0], c[1], c[2], z[0], z[1]);
+        else split_a(c[0], c[1], z[0], z[1]);
+    }
+    constexpr int kLast = kExact ? 2 : 1;   // the smallest terms first
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint32_t kb[4];
+        uint32_t kb[4], qb[4];
         ldsm4t(kb, step(kt, i));
+        if (kTwo) ldsm4t(qb, step(qt, i));
+        float d[2][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int n = kLast; n >= 0; --n) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[2 * i + u][e] *= factor;
-            if (kExact) mma(S[2 * i + u], a2, kb[2 * u], kb[2 * u + 1]);
+            for (int u = 0; u < 2; ++u) {
+                if (n == kLast) mma0(d[u], a[n], kb[2 * u], kb[2 * u + 1]);
+                else mma(d[u], a[n], kb[2 * u], kb[2 * u + 1]);
+            }
+            if (kTwo)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) mma(d[u], c[n], qb[2 * u], qb[2 * u + 1]);
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) mma(S[2 * i + u], a1, kb[2 * u], kb[2 * u + 1]);
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) mma(S[2 * i + u], a0, kb[2 * u], kb[2 * u + 1]);
+            for (int e = 0; e < 4; ++e) S[2 * i + u][e] = fmaf(S[2 * i + u][e], factor, d[u][e]);
     }
 }
 
