@@ -631,9 +631,13 @@ gated_delta_bwd_out_tc_kernel(const __grid_constant__ Args p) {
         }
         good = ready();   // also: this head's tiles may be overwritten
     }
-    // late: NaN results; the products last issued may be running still and get a second's time
+    // late: NaN results; the products issued may be running still, on tiles and columns that others
+    // get next.  They have a second's time: the group last committed, then what went out behind it
+    // (Q K^T, behind the first group), for which a commit of its own answers.
     if (!good) {
         (void)ptx::mbar_wait(&s.done, phase ^ 1, kDrain);
+        if (issuer && ptx::elect_one()) ptx::mma_commit(&s.done);
+        (void)ptx::mbar_wait(&s.done, phase, kDrain);
         const float nan = __int_as_float(0x7fffffff);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
