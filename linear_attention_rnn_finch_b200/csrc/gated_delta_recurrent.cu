@@ -106,7 +106,7 @@ gated_delta_recurrent_kernel(const float* __restrict__ q, const float* __restric
 #pragma unroll
         for (int j = 0; j < kJ; ++j) *reinterpret_cast<float4*>(&s.v[tv][cv + 32 * j]) = rv[j];
         if (tid < kTile) {
-            s.w[tid] = decay_from_logit(rw);
+            s.w[tid] = gdr::decay(rw);
             s.b[tid] = rb;
         }
         __syncthreads();   // the buffer's last readers passed the barrier of tile n - 1
@@ -188,7 +188,7 @@ gated_delta_decode_kernel(const IO* __restrict__ q, const IO* __restrict__ k,
     float4 s[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) s[m] = __ldcs(&S[(r0 + 16 * m) * (D / 4) + c]);
-    const float w = decay_from_logit(to_f32(omega[bh])), bt = to_f32(beta[bh]);
+    const float w = gdr::decay(to_f32(omega[bh])), bt = to_f32(beta[bh]);
     if (tid < D) {
         const float qv = to_f32(q[kh + tid]), kv = to_f32(k[kh + tid]);
         sq[tid] = qv;

@@ -81,3 +81,26 @@ def test_initial_state_gradient(kind, B, H, HK, T):
         de = beta[:, t, :, None] * torch.einsum("bhij,bhi->bhj", G, k[:, t])
         G = (G - torch.einsum("bhi,bhj->bhij", k[:, t], de)) * w[:, t, :, None, None]
     assert off(got, G) <= tolerance(kind, T)
+
+
+@pytest.mark.parametrize("B,H,HK,T", [(1, 2, 1, 4096), (1, 160, 2, 1024)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_final_state_token_by_token(kind, B, H, HK, T):
+    """The fp32 prefill: a token's decay and update round each entry twice, 16 tokens 32 times by 2^-25
+    on average, sqrt(32) 2^-25 = 2.9 x 2^-24 in all: within the tolerance of the others."""
+    p = {n: x.float() for n, x in long_problem(kind, B, T, H, HK).items()}
+    _, s = gw.gated_delta_prefill(*args(p), scale=SCALE)
+    _, want = ref.prefill(*[a.double() for a in args(p)], scale=SCALE)
+    assert off(s, want) <= tolerance(kind, T, cut=False)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+@pytest.mark.parametrize("kind", ["slow", "full"])
+def test_state_of_a_long_decode(kind, dtype):
+    B, H, HK, T = 2, 4, 2, 1024
+    p = {n: (x.to(dtype) if n != "s0" else x) for n, x in long_problem(kind, B, T, H, HK).items()}
+    s = p["s0"].clone()
+    for t in range(T):
+        gw.gated_delta_decode_step(*[p[n][:, t].contiguous() for n in ("q", "k", "v", "omega", "beta")], s, scale=SCALE)
+    _, want = ref.prefill(*[a.double() for a in args(p)], scale=SCALE)
+    assert off(s, want) <= tolerance(kind, T, cut=False)
