@@ -1,0 +1,48 @@
+"""Group norm with an activation where a thread adds up many values: sets of lanes that walk
+several rows, statistics over hundreds of positions behind an outlying first one, and parameter
+gradients over hundreds of thousands of n."""
+import pytest
+import torch
+
+import linear_attention_rnn_finch_b200 as gw
+from tests.test_group_norm_act_gpu import BF16, DEV, F32, OWN, check, close, problem
+
+pytestmark = pytest.mark.gpu
+
+
+def most_streams(C, groups, ctas):
+    """Rows that are walked at once: sets of lanes, of 256 / lanes a block, over the groups."""
+    per = C // groups
+    units = per // 8 if per % 8 == 0 else per
+    lanes = min(32, 1 << (units - 1).bit_length())
+    return -(-148 * ctas * (256 // lanes) // groups)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("act,gate", [("silu", True), ("silu", False), ("none", True), ("none", False)])
+@pytest.mark.parametrize("groups,per,N", [(40, 64, 2500), (40, 24, 2500), (32, 1032, 301), (24, 10, 1999),
+                                          (16, 100, 1403), (16, 40, 5003), (8, 520, 2503), (8, 300, 2503)])
+def test_rows_walked_by_one_set(groups, per, N, act, gate, dtype):
+    """More rows than are walked at once (8 blocks an SM forward, 3 in the gradient) and no
+    multiple of them, so that some sets end a row early."""
+    C = groups * per
+    for ctas in (3, 8):
+        streams = most_streams(C, groups, ctas)
+        assert N > streams and N % streams
+    check(problem(40 + per, (N, C), dtype, gate), groups, act)
+
+
+def test_first_position_outlies_many_positions():
+    """A thread adds up 1000 positions, the first of which, from whose value the others' differences
+    start, is 1000 deviations away: the same tolerance as for a few positions a thread."""
+    N, L, C, groups = 300, 1000, 2048, 32
+    g = torch.Generator(device=DEV).manual_seed(7)
+    x = torch.empty(N, L, C, device=DEV).normal_(0, 1.5, generator=g)
+    x[:, 0] = 1500.0
+    ga, be = torch.ones(C, device=DEV), torch.zeros(C, device=DEV)
+    y = gw.group_norm_act(x, ga, be, 1e-3, groups=groups, act="none")
+    for n in (0, N - 1):
+        h = x[n].double().view(L, groups, -1)
+        var, mean = torch.var_mean(h, (0, 2), correction=0, keepdim=True)
+        want = ((h - mean) / torch.sqrt(var + 1e-3)).view(L, C)
+        close(y[n], want.cpu(), OWN, f"y[{n}]")
