@@ -46,3 +46,25 @@ def test_first_position_outlies_many_positions():
         var, mean = torch.var_mean(h, (0, 2), correction=0, keepdim=True)
         want = ((h - mean) / torch.sqrt(var + 1e-3)).view(L, C)
         close(y[n], want.cpu(), OWN, f"y[{n}]")
+
+
+@pytest.mark.parametrize("N,L", [(400_000, 2), (3000, 300)])
+def test_parameter_gradients_of_many(N, L):
+    """dbeta is the sum of N L values of one sign, dgamma that of as many products.  A row of partial
+    sums holds at most 2 + 128 additions, runs of them 32 more, each off by 2^-25 on average with
+    independent signs: under sqrt(162) 2^-25 = 3.8e-7 of the magnitudes; joined in 64 bits it stays
+    that however many there are.  Rounding the result adds 2^-24, and the largest of 32 columns may
+    be twice the average."""
+    C, groups = 16, 2
+    g = torch.Generator(device=DEV).manual_seed(N)
+    x = torch.randn(N, L, C, generator=g, device=DEV)
+    dy = 1 + torch.rand(N, L, C, generator=g, device=DEV)
+    ga, be = torch.ones(C, device=DEV), torch.zeros(C, device=DEV)
+    _, dgamma, dbeta, _ = gw.group_norm_act_backward(x, ga, be, 1e-3, dy, groups=groups, act="none")
+    d = dy.double()
+    h = x.double().view(N, L, groups, -1)
+    var, mean = torch.var_mean(h, (1, 3), correction=0, keepdim=True)
+    h = ((h - mean) / torch.sqrt(var + 1e-3)).view(N, L, C)
+    for got, terms in ((dbeta, d), (dgamma, d * h)):
+        off = (got.double() - terms.sum((0, 1))).abs() / terms.abs().sum((0, 1))
+        assert float(off.max()) <= 9e-7, float(off.max())
