@@ -140,9 +140,17 @@ wkv_status gated_delta_backward(const void* q, const void* k, const void* v, con
                                 size_t workspace_bytes, void* stream) {
     wkv_status s = check_gdr_sizes(B, T, H, HK, D, io, scale);
     if (s != WKV_OK) return s;
-    if (B == 0 || H == 0) return WKV_OK;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const size_t es = io_size(io), bt = (size_t)B * T;
+    if (B == 0 || H == 0) {   // key heads without value heads: sums of nothing
+        const size_t kb = bt * HK * D * es;
+        if (kb == 0) return WKV_OK;
+        const Arg args[] = {{q, kb, false, false}, {k, kb, false, false}, {dq, kb, true, true}, {dk, kb, true, true}};
+        if ((s = check_args(args, 4)) != WKV_OK) return s;
+        if (injected("launch")) return WKV_ERR_CUDA;
+        const cudaError_t e = cudaMemsetAsync(dq, 0, kb, st);
+        return from_cuda(e != cudaSuccess ? e : cudaMemsetAsync(dk, 0, kb, st));
+    }
     const size_t kb = bt * HK * D * es, vb = bt * H * D * es, gb = bt * H * es;
     const size_t sb = (size_t)B * H * D * D * sizeof(float);
     const size_t need = gated_delta_backward_workspace_bytes(B, T, H, HK, D, io);

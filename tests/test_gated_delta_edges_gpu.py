@@ -1,11 +1,44 @@
 """Edges of the gated delta rule's and the norm's calls on the GPU."""
+import ctypes
+
 import pytest
 import torch
 
 import linear_attention_rnn_finch_b200 as gw
-from tests.test_gated_delta_gpu import BF16, SCALE, args, problem
+from linear_attention_rnn_finch_b200 import binding as bd
+from tests.test_gated_delta_gpu import BF16, DEV, F32, SCALE, args, problem
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_key_heads_without_value_heads(dtype):
+    """dq and dk are each key head's sum over no value heads: zeros, whatever lay there before."""
+    L = bd.load()
+    B, T, HK = 2, 70, 3
+    q, k = (torch.randn(B, T, HK, 64, device=DEV).to(dtype) for _ in range(2))
+    dq, dk = (torch.full_like(q, float("nan")) for _ in range(2))
+    at = lambda t: ctypes.c_void_p(t.data_ptr())
+
+    def call(a, b):
+        st = L.gated_delta_backward(at(q), at(k), None, None, None, 1.0, None, None, None, a, b, None, None, None,
+                                    None, B, T, 0, HK, 64, bd._io(dtype), None, 0, None)
+        torch.cuda.synchronize()
+        return st
+
+    assert call(None, at(dk)) == bd.WKV_ERR_INVALID_ARG and call(at(q), at(dk)) == bd.WKV_ERR_INVALID_ARG
+    assert call(at(dq), at(dq)) == bd.WKV_ERR_INVALID_ARG
+    assert bool(torch.isnan(dq).all()) and bool(torch.isnan(dk).all())
+    assert call(at(dq), at(dk)) == bd.WKV_OK
+    assert bool((dq == 0).all()) and bool((dk == 0).all())
+    v, om = torch.empty(B, T, 0, 64, device=DEV, dtype=dtype), torch.empty(B, T, 0, device=DEV, dtype=dtype)
+    held = [torch.full_like(q, float("nan")) for _ in range(4)]
+    torch.cuda.synchronize()
+    del held
+    out = gw.gated_delta_backward(q, k, v, om, om.clone(), None, v.clone())
+    assert bool((out[0] == 0).all()) and bool((out[1] == 0).all())
+    y, s = gw.gated_delta_prefill(q, k, v, om, om.clone())
+    assert y.shape == (B, T, 0, 64) and s.shape == (B, 0, 64, 64)
 
 
 def test_expired_waits_on_a_full_device():
