@@ -48,6 +48,8 @@ wkv_status check_gdr_sizes(int B, int T, int H, int HK, int D, wkv_dtype io, flo
     if (B < 0 || T < 0 || H < 0 || HK < 0 || !valid_io(io) || !isfinite(scale)) return WKV_ERR_INVALID_ARG;
     if (H > 0 && (HK == 0 || H % HK != 0)) return WKV_ERR_INVALID_ARG;
     if (D != kHeadSizeApi) return WKV_ERR_UNSUPPORTED;
+    // token numbers are ints and run up to three blocks of 64 past the end
+    if (T > 2147483647 - 256) return WKV_ERR_UNSUPPORTED;
     // one CTA per head, or per head and chunk of 64 tokens
     if ((double)B * H * (T / 64 + 1) > 2147483647.0) return WKV_ERR_UNSUPPORTED;
     return WKV_OK;
