@@ -685,6 +685,10 @@ def _workspace(workspace, need, device):
         if need == 0:
             return None, None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if not workspace.is_contiguous():   # its elements are counted as bytes that are there
+        raise ValueError("workspace must be contiguous")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
