@@ -666,6 +666,12 @@ def _optional(name, t, device, dtype, shape):
     return None if t is None else _is(name, t, device, dtype, shape)
 
 
+def _fits(name, n):
+    """The library's sizes are C ints, into which ctypes would cut a larger one without a word."""
+    if n > 0x7FFFFFFF:
+        raise ValueError(f"{name} {n} does not fit in 32 bits")
+
+
 def _call(what, fn, device, stream, *args):
     """fn(*args, stream) with `device` current; raises on an error status."""
     index = device.index
@@ -712,6 +718,7 @@ def _gdr_args(q, k, v, omega, beta, lead):
         raise ValueError("q and v must be " + ("[B, T, heads, D]" if lead == 2 else "[B, heads, D]"))
     shape, H = q.shape, v.shape[-2]
     front, HK, D = shape[:lead], shape[-2], shape[-1]
+    _fits("head size", D)
     if H and (HK == 0 or H % HK):
         raise ValueError(f"the {H} value heads must be a multiple of the {HK} key heads")
     dev, dt = q.device, q.dtype
@@ -809,6 +816,7 @@ def _gn_args(x, gamma, beta, groups, act, gate):
     N, C, L = shape[0], shape[-1], 1
     if C == 0 or groups <= 0 or C % groups:
         raise ValueError(f"the {C} channels must be a positive multiple of groups ({groups})")
+    _fits("channels", C)
     code = ACTS.get(act)
     if code is None:
         raise ValueError(f"unknown activation {act!r}; expected one of {sorted(ACTS)}")

@@ -37,3 +37,9 @@ def test_workspace_must_be_dense():
     ws, at, n = bd._workspace(torch.empty(100, dtype=torch.float32), 256, "cpu")
     assert at == ws.data_ptr() and n == 400
     assert bd._workspace(None, 0, "cpu") == (None, None, 0)
+
+
+def test_sizes_that_ctypes_would_cut():
+    bd._fits("channels", INT_MAX)
+    with pytest.raises(ValueError):
+        bd._fits("channels", 2 ** 32 + 64)

@@ -41,6 +41,17 @@ def test_key_heads_without_value_heads(dtype):
     assert y.shape == (B, T, 0, 64) and s.shape == (B, 0, 64, 64)
 
 
+def test_channels_beyond_32_bits_are_refused():
+    """2^32 + 64 channels are 64 in a C int."""
+    C = 2 ** 32 + 64
+    x = torch.empty(1, C, device=DEV, dtype=BF16)
+    p = torch.empty(C, device=DEV)
+    with pytest.raises(ValueError):
+        gw.group_norm_act(x, p, p.clone(), groups=1)
+    with pytest.raises(ValueError):
+        gw.group_norm_act_backward(x, p, p.clone(), 1e-5, x.clone(), groups=1)
+
+
 def test_expired_waits_on_a_full_device():
     """With no cycles to wait in, four times: blocks are NaN or what they are, with two of them on
     an SM whose neighbours leave early, and the calls after it are whole."""
