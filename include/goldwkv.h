@@ -370,7 +370,9 @@ wkv_status gold_decompress(const void *x0, const void *c, const void *w_ku, cons
  *   v, y        [B][T][H][D]
  *   omega, beta [B][T][H]       omega = -inf: no decay; +inf: the state is forgotten.  A token
  *                               with beta = 0 writes nothing, and with omega = -inf as well it
- *                               leaves the state as it is (padding; its other inputs finite)
+ *                               leaves the state as it is (padding; zeros will do as its q, k
+ *                               and v, and so does anything whose products stay finite: k within
+ *                               the bounds of any other token's)
  *   state       [B][H][D][D] fp32
  * Tokens are worked on in groups: a NaN or an infinity in one reaches its head's outputs from it
  * on, as the recurrence has it, and may reach those of the 63 tokens before it.

@@ -1,4 +1,5 @@
-"""Edges of the gated delta rule's and the norm's calls on the GPU."""
+"""Edges of the gated delta rule's and the norm's calls on the GPU: key heads without value heads,
+sizes beyond 32 bits, padding, and waits that expire on a full device."""
 import ctypes
 
 import pytest
@@ -6,6 +7,8 @@ import torch
 
 import linear_attention_rnn_finch_b200 as gw
 from linear_attention_rnn_finch_b200 import binding as bd
+from tests import gated_delta_ref as ref
+from tests.gated_delta_ref import OWN, c64, close
 from tests.test_gated_delta_gpu import BF16, DEV, F32, SCALE, args, problem
 
 pytestmark = pytest.mark.gpu
@@ -50,6 +53,30 @@ def test_channels_beyond_32_bits_are_refused():
         gw.group_norm_act(x, p, p.clone(), groups=1)
     with pytest.raises(ValueError):
         gw.group_norm_act_backward(x, p, p.clone(), 1e-5, x.clone(), groups=1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("side", ["left", "right"])
+def test_padding_on_either_side(side, dtype):
+    """Tokens with beta = 0 and omega = -inf, q, k and v zeros or another token's: the others' outputs
+    and the state are those of the recurrence without them."""
+    B, T, n = 2, 150, 37
+    p = problem(700, B, T, 4, 2, dtype)
+    for fill in ("zeros", "others"):
+        pad = {}
+        for name in ("q", "k", "v", "omega", "beta"):
+            x = p[name][:, :n].clone()
+            if name == "omega":
+                x.fill_(-float("inf"))
+            elif name == "beta" or fill == "zeros":
+                x.zero_()
+            pad[name] = torch.cat([x, p[name]] if side == "left" else [p[name], x], 1).contiguous()
+        pad["s0"] = p["s0"]
+        y0, s0 = ref.prefill(*[c64(a) for a in args(p)], scale=SCALE)
+        y1, s1 = gw.gated_delta_prefill(*args(pad), scale=SCALE)
+        own = y1[:, n:] if side == "left" else y1[:, :T]
+        close(own.contiguous(), y0, OWN[dtype], "y")
+        close(s1, s0, OWN[dtype], "state")
 
 
 def test_expired_waits_on_a_full_device():
