@@ -579,32 +579,35 @@ group_norm_full_rows_bwd_kernel(const IO* __restrict__ x, const IO* __restrict__
 }
 
 // dgamma[c], dbeta[c] = the sums of `rows` partial rows ([rows][2][C]), in a fixed order: 32
-// columns a CTA, kWarps row lanes each, joined through shared memory.  Runs of 32 rows in 32 bits,
-// their sums in 64: with a row for each n a lane adds up tens of thousands, which in 32 bits alone
-// leave 3e-6 of 800,000 values of one sign (each row in 64 bits: 5 % of the call, [8000, 4, 320]).
+// columns a CTA, kWarps row lanes each, joined through shared memory.  A lane takes eight rows at a
+// time, all their loads in flight, and carries on what rounding takes from its sum (Kahan's): with
+// a row for each n it adds up tens of thousands, which plainly leave 3e-6 of 800,000 values of one
+// sign.
 template <int kWarps>
 __device__ __forceinline__ void sum_params(const float* __restrict__ part, long rows, int C, int cta,
                                            float* __restrict__ dgamma, float* __restrict__ dbeta) {
-    __shared__ double red[kWarps][33];
+    __shared__ float red[kWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i = cta * 32 + lane;   // column of the 2 C
-    double sum = 0.0;
+    float sum = 0.f, lost = 0.f;
     if (i < 2 * C)
-        for (long r = warp; r < rows;) {
-            const long end = min(rows, r + 32L * kWarps);
-            float acc = 0.f;
-#pragma unroll 8
-            for (; r < end; r += kWarps) acc += part[(size_t)r * 2 * C + i];
-            sum += (double)acc;
+        for (long r = warp; r < rows; r += 8 * kWarps) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = r + u * kWarps < rows ? part[(size_t)(r + u * kWarps) * 2 * C + i] : 0.f;
+            const float add = (((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]))) - lost;
+            const float next = sum + add;
+            lost = (next - sum) - add;
+            sum = next;
         }
     red[warp][lane] = sum;
     __syncthreads();
     if (warp == 0 && i < 2 * C) {
-        double t = 0.0;
+        float t = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) t += red[w][lane];
-        if (i < C) dgamma[i] = (float)t;
-        else dbeta[i - C] = (float)t;
+        if (i < C) dgamma[i] = t;
+        else dbeta[i - C] = t;
     }
 }
 constexpr int kParamWarps = 32;   // few rows a warp: the loads' latency is all that counts

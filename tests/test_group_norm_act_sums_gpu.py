@@ -51,10 +51,10 @@ def test_first_position_outlies_many_positions():
 @pytest.mark.parametrize("N,L", [(400_000, 2), (3000, 300)])
 def test_parameter_gradients_of_many(N, L):
     """dbeta is the sum of N L values of one sign, dgamma that of as many products.  A row of partial
-    sums holds at most 2 + 128 additions, runs of them 32 more, each off by 2^-25 on average with
-    independent signs: under sqrt(162) 2^-25 = 3.8e-7 of the magnitudes; joined in 64 bits it stays
-    that however many there are.  Rounding the result adds 2^-24, and the largest of 32 columns may
-    be twice the average."""
+    sums holds at most 2 + 128 additions, eight rows and the warps' sums 3 + 32 more, each off by
+    2^-25 on average with independent signs: under sqrt(165) 2^-25 = 3.8e-7 of the magnitudes; with
+    what rounding takes from the running sum carried on it stays that however many there are.
+    Rounding the result adds 2^-24, and the largest of 32 columns may be twice the average."""
     C, groups = 16, 2
     g = torch.Generator(device=DEV).manual_seed(N)
     x = torch.randn(N, L, C, generator=g, device=DEV)
