@@ -7,9 +7,10 @@ into ``linear_attention_rnn_finch_b200/libgoldwkv.so`` (CUDA runtime linked stat
 the library does not depend on a particular libcudart.so being on the loader path).
 
 ``--debug`` builds ``libgoldwkv_debug.so`` instead (objects under ``_build_debug/``), with
-``-DGW_DEBUG``: the chunked kernels check the coordinates of every copy and store and the
-index ranges of their threads on the device; a failed check sets bit 1 of the call's
-status word and skips the access.  Same ABI, slower; for tests and debugging.
+``-DGW_DEBUG``: the WKV recurrence's chunked kernels check the coordinates of every copy and
+store and the index ranges of their threads on the device; a failed check sets bit 1 of the
+call's status word and skips the access.  (The gated delta rule's calls and the norm's have no
+status word and no such checks.)  Same ABI, slower; for tests and debugging.
 """
 from __future__ import annotations
 
