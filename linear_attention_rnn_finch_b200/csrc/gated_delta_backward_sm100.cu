@@ -685,7 +685,7 @@ cudaError_t run(bool first, Kernel kernel, unsigned grid, int threads, size_t sm
 
 }  // namespace
 
-static GdrSegments segments(int B, int T, int H) { return gdr_segments(B, T, H, 2, 3, 3.2f, 2.8f); }
+static GdrSegments segments(int B, int T, int H) { return gdr_segments(B, T, H, 2, 3, 3.4f, 3.0f); }
 
 size_t gdr_backward_tc_bytes(int B, int T, int H) {
     const size_t heads = (size_t)B * H;

@@ -203,7 +203,7 @@ gated_delta_maps_kernel(const __grid_constant__ Args p) {
 }
 
 Segments segments(int B, int T, int H) {
-    const GdrSegments g = gdr_segments(B, T, H, 1, 2, 2.7f, 2.0f);
+    const GdrSegments g = gdr_segments(B, T, H, 1, 2, 2.9f, 2.3f);
     return Segments{g.count, g.blocks, nullptr, nullptr};
 }
 
