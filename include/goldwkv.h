@@ -384,7 +384,8 @@ wkv_status gold_decompress(const void *x0, const void *c, const void *w_ku, cons
  * gated_delta_prefill: T tokens from state_in (NULL: zero).  state_out [B][H][D][D] or NULL (not
  * written); it may equal state_in.  No other overlap of an output.  T == 0: state_out receives
  * state_in, or zeros.  workspace: at least gated_delta_prefill_workspace_bytes(...) bytes (may be
- * NULL when that is 0).
+ * NULL when that is 0); bf16 calls of few heads need 32 KB a head and segment of the sequence, the
+ * others none.
  */
 size_t gated_delta_prefill_workspace_bytes(int B, int T, int H, int HK, int D, wkv_dtype io);
 wkv_status gated_delta_prefill(const void *q, const void *k, const void *v, const void *omega,
@@ -404,7 +405,9 @@ wkv_status gated_delta_decode_step(const void *q, const void *k, const void *v, 
  * state's gradient, NULL: zero).  Outputs: dq, dk [B][T][HK][D] io (each key head's the sum over
  * its value heads), dv [B][T][H][D] io, domega, dbeta [B][T][H] io, dstate_in [B][H][D][D] fp32
  * or NULL (not computed).  No output may overlap an input, another output or the workspace.
- * T == 0: dstate_in = dstate_out, or zeros.  The same inputs give the same bits (no atomics).
+ * T == 0: dstate_in = dstate_out, or zeros.  H == 0: dq and dk are zeros.  The same inputs give
+ * the same bits (no atomics).  The workspace is large, 1 KB a token and head with bf16 and 1.25 KB
+ * with fp32 I/O (1.07 GB at B = 8, T = 4096, H = 32); calls in one stream can share one.
  * A device-side wait that expires (bf16; about a second, where microseconds are due) leaves NaN
  * in the dq, dk, domega and dbeta of its 64 tokens.
  */

@@ -2,7 +2,7 @@
 // leave and wait on the device for its end, so that less time passes between two launches (two in
 // B8 T4093 C320 of group norm 20.9 -> 18.9 us, four of the fp32 backward of the gated delta rule
 // at B2 T333 H4 78 -> 72).  Placed earlier, while all of the present one's still run, they share
-// SMs that they would have to themselves: 8 heads of 8192 tokens 74 us instead of 68.
+// SMs that they would have to themselves: 8 heads of 8192 tokens took a tenth longer.
 //
 // A call's first launch is an ordinary one, which starts after all that came before it in its
 // stream.  A later one goes through launch_next; all of its threads call previous_ended before

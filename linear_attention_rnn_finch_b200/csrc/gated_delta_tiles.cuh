@@ -33,13 +33,14 @@
 // way, 1.7e-3.  Three parts there take B8 T4096 H32 a tenth longer.
 // B8 T4096 H32 takes 353 us so, with two parts against K 322, with two throughout 287.
 //
-// mma.sync, not tcgen05: the chain's products are 16 x 16 x 64 and smaller and each needs the one
-// before it, which as tcgen05.mma is a round through shared memory, a barrier, a commit and TMEM
-// loads (a group of 64 x 64 x 64 products takes 1000 cycles and more in the backward's second
-// launch), against 21 cycles for a register-to-register mma.sync, one every 8 a scheduler.  What
-// bounds a chain is its schedulers: an mma.sync keeps the FP32 pipe's dispatch for about 6 of its 8
+// mma.sync: the chain's products are 16 x 16 x 64 and smaller and each needs the one before it, 21
+// cycles from registers to registers, one every 8 a scheduler.  tcgen05 would take the 64-token form:
+// three groups of products a block (K S, T F, K^T E), each a round through shared memory, a barrier, a
+// commit and TMEM loads, about 1000 cycles in the backward's second launch, against 5500 for the
+// four sub-chunks of a block here; that form has not been built.  What bounds a chain here is its
+// schedulers: an mma.sync keeps the FP32 pipe's dispatch for about 6 of its 8
 // cycles, so the 82 of a sub-chunk and the 400 instructions beside them hardly overlap (1370 cycles
-// a sub-chunk where the tensor pipe needs 660; a second CTA on the SM adds an eighth).
+// a sub-chunk where the tensor pipe needs 660; a second CTA on the SM adds a twentieth).
 #pragma once
 
 #include "gated_delta.h"
