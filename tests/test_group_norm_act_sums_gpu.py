@@ -32,20 +32,34 @@ def test_rows_walked_by_one_set(groups, per, N, act, gate, dtype):
     check(problem(40 + per, (N, C), dtype, gate), groups, act)
 
 
-def test_first_position_outlies_many_positions():
-    """A thread adds up 1000 positions, the first of which, from whose value the others' differences
-    start, is 1000 deviations away: the same tolerance as for a few positions a thread."""
-    N, L, C, groups = 300, 1000, 2048, 32
+def statistics_of_many(C, groups, own, fill):
+    """y of [300, 1000, C], where a thread adds up 1000 positions, against 64 bits."""
+    N, L = 300, 1000
     g = torch.Generator(device=DEV).manual_seed(7)
     x = torch.empty(N, L, C, device=DEV).normal_(0, 1.5, generator=g)
-    x[:, 0] = 1500.0
+    fill(x)
     ga, be = torch.ones(C, device=DEV), torch.zeros(C, device=DEV)
     y = gw.group_norm_act(x, ga, be, 1e-3, groups=groups, act="none")
     for n in (0, N - 1):
         h = x[n].double().view(L, groups, -1)
         var, mean = torch.var_mean(h, (0, 2), correction=0, keepdim=True)
         want = ((h - mean) / torch.sqrt(var + 1e-3)).view(L, C)
-        close(y[n], want.cpu(), OWN, f"y[{n}]")
+        close(y[n], want.cpu(), own, f"y[{n}]")
+
+
+@pytest.mark.parametrize("C,groups", [(2048, 32), (250, 10)])
+@pytest.mark.parametrize("at", [0, 500])
+def test_a_position_outlies_many(at, C, groups):
+    """One position, the first, from whose value the others' differences start, or one amid them, is
+    1000 deviations away: the same tolerance as for a few positions a thread."""
+    statistics_of_many(C, groups, OWN, lambda x: x[:, at].fill_(1500.0))
+
+
+@pytest.mark.parametrize("C,groups", [(2048, 2048), (250, 10)])
+def test_mean_far_from_zero_over_many(C, groups):
+    """Mean 1000 at deviation 1.5 joined 16 times: one step of the mean, 2^-24 x 1000 = 6e-5, over the
+    deviation is 4e-5 of h, whose largest is above 4: 1e-4, as for few positions."""
+    statistics_of_many(C, groups, 1e-4, lambda x: x.add_(1000.0))
 
 
 @pytest.mark.parametrize("N,L", [(400_000, 2), (3000, 300)])
