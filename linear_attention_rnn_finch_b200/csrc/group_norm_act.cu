@@ -597,7 +597,7 @@ __device__ __forceinline__ void sum_params(const float* __restrict__ part, long 
             for (int u = 0; u < 8; ++u) v[u] = r + u * kWarps < rows ? part[(size_t)(r + u * kWarps) * 2 * C + i] : 0.f;
             const float add = (((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]))) - lost;
             const float next = sum + add;
-            lost = (next - sum) - add;
+            lost = isfinite(next) ? (next - sum) - add : 0.f;   // an infinite sum stays one
             sum = next;
         }
     red[warp][lane] = sum;

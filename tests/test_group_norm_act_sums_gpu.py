@@ -82,3 +82,20 @@ def test_parameter_gradients_of_many(N, L):
     for got, terms in ((dbeta, d), (dgamma, d * h)):
         off = (got.double() - terms.sum((0, 1))).abs() / terms.abs().sum((0, 1))
         assert float(off.max()) <= 9e-7, float(off.max())
+
+
+@pytest.mark.parametrize("shape", [(3000, 2, 32), (70_000, 32)])
+def test_infinite_gradients_stay_in_their_channel(shape):
+    """dy infinite in one place of a channel: its dbeta is that infinity, wherever the place comes in the
+    sum, and the other channels' sums are those without it."""
+    p = problem(60, shape, F32, False)
+    at = p["dy"].view(-1, 32)
+    call = lambda: gw.group_norm_act_backward(p["x"], p["gamma"], p["beta"], 1e-3, p["dy"], groups=4, act="none")[1:3]
+    clean = call()
+    at[5, 3], at[2999, 20] = float("inf"), -float("inf")
+    dgamma, dbeta = call()
+    assert float(dbeta[3]) == float("inf") and float(dbeta[20]) == -float("inf")
+    assert bool(torch.isinf(dgamma[[3, 20]]).all())
+    keep = [c for c in range(32) if c not in (3, 20)]
+    for got, want in zip((dgamma, dbeta), clean):
+        assert torch.equal(got[keep], want[keep])
